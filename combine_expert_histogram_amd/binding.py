@@ -26,7 +26,8 @@ EXPORTS = ("moe_status_string", "moe_capacity", "moe_route_layout_workspace", "m
            "moe_quant_dispatch", "moe_grouped_gemm1_workspace", "moe_grouped_gemm1",
            "moe_quant_dispatch_mx", "moe_grouped_gemm1_mx", "moe_silu_mul_quant",
            "moe_grouped_gemm2_workspace", "moe_grouped_gemm2", "moe_silu_mul_quant_mx",
-           "moe_grouped_gemm2_mx", "moe_combine")
+           "moe_grouped_gemm2_mx", "moe_combine", "moe_route_topk", "moe_matvec",
+           "moe_few_token_layer_workspace", "moe_few_token_layer")
 
 
 class MoeError(RuntimeError):
@@ -40,6 +41,11 @@ class moe_dims(ctypes.Structure):
                 ("top_k", ctypes.c_int32), ("num_experts", ctypes.c_int32),
                 ("expert_begin", ctypes.c_int32), ("num_local_experts", ctypes.c_int32),
                 ("hidden", ctypes.c_int32)]
+
+
+class moe_weight(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("group", ctypes.c_int32), ("data", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p)]
 
 
 @dataclass(frozen=True)
@@ -90,6 +96,11 @@ def lib() -> ctypes.CDLL:
             "moe_silu_mul_quant_mx": (I32, [D, I32, P, P, P, P, P]),
             "moe_grouped_gemm2_mx": (I32, [D, I32] + [P] * 8 + [P, SZ, P]),
             "moe_combine": (I32, [D, I32, P, I64, P, P, P, P]),
+            "moe_route_topk": (I32, [D, P, I32, I64, I32, ctypes.c_float, P, P, P]),
+            "moe_matvec": (I32, [I32, I32, I32, P, I64, ctypes.POINTER(moe_weight), P, I64, P]),
+            "moe_few_token_layer_workspace": (I32, [D, I32, ctypes.POINTER(SZ)]),
+            "moe_few_token_layer": (I32, [D, I32, P, P, P, ctypes.POINTER(moe_weight),
+                                          ctypes.POINTER(moe_weight), P, P, SZ, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -400,4 +411,208 @@ def grouped_gemm2_mx(d: Dims, inter: int, h, h_scale, lay: dict, topk_w, w2_e4m3
 def combine(d: Dims, width: int, y_bf16, assign_row, topk_w, out=None):
     out = torch.empty((max(d.T, 1), width), dtype=torch.bfloat16, device=y_bf16.device) if out is None else out
     moe_combine(d, width, y_bf16, assign_row, topk_w, out)
+    return out
+
+
+# ---------------------------------------------------------------- few tokens
+WEIGHT_FORMATS = {"e4m3": 0, "e4m3_mx": 1, "e2m1_mx": 2, "int4": 3}
+_BF16_BITS = (torch.bfloat16, torch.int16, torch.uint16)
+_PACKED = (torch.int32, torch.uint32)
+
+
+class Weight:
+    """A weight matrix [n, k], or `experts` of them one after the other, in one of the header's formats
+    (moe_weight_format): "e4m3", "e4m3_mx", "e2m1_mx" or "int4".  Holds its tensors and checks them once."""
+
+    def __init__(self, fmt: str, n: int, k: int, data, scale, zero=None, group: int = 128, experts: int = 1):
+        if fmt not in WEIGHT_FORMATS:
+            raise ValueError(f"fmt must be one of {sorted(WEIGHT_FORMATS)}, got {fmt!r}")
+        if n < 4 or n % 4 or k < 128 or k % 128 or experts < 1:
+            raise ValueError(f"n must be a multiple of 4, k of 128 and experts positive, got {n}, {k}, {experts}")
+        if fmt == "e4m3" and n % 128:
+            raise ValueError("an e4m3 weight's n must be a multiple of 128")
+        if fmt == "int4" and group not in (32, 64, 128):
+            raise ValueError(f"group must be 32, 64 or 128, got {group}")
+        if fmt != "int4" and zero is not None:
+            raise ValueError("zero points belong to int4 weights")
+        numel, blocks = experts * n * k, experts * n * (k // 128)
+        self._tensor(data, "data", (torch.uint8,), numel // (2 if fmt in ("e2m1_mx", "int4") else 1))
+        if fmt == "e4m3":
+            self._tensor(scale, "scale", (torch.float32,), blocks // 128)
+        elif fmt == "int4":
+            self._tensor(scale, "scale", _BF16_BITS, numel // group)
+        else:
+            self._tensor(scale, "scale", _PACKED, blocks)
+        if zero is not None:
+            self._tensor(zero, "zero", (torch.uint8,), numel // group)
+        if len({t.device for t in (data, scale, zero) if t is not None}) != 1:
+            raise ValueError("data, scale and zero must be on one device")
+        self.fmt, self.n, self.k, self.group, self.experts = fmt, n, k, group, experts
+        self.data, self.scale, self.zero, self.device = data, scale, zero, data.device
+        self._c = moe_weight(WEIGHT_FORMATS[fmt], group if fmt == "int4" else 0, data.data_ptr(), scale.data_ptr(),
+                             None if zero is None else zero.data_ptr())
+
+    @staticmethod
+    def _tensor(t, name, dtypes, numel):
+        if t.dtype not in dtypes:
+            raise ValueError(f"{name} must be one of {dtypes}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.numel() != numel:
+            raise ValueError(f"{name} must hold {numel} elements, got {t.numel()}")
+        if t.data_ptr() % 16:
+            raise ValueError(f"{name} must be 16-byte aligned")
+
+    def c(self):
+        return ctypes.byref(self._c)
+
+
+def _blocks_first(t: torch.Tensor, per_block: int) -> torch.Tensor:
+    """[.., n, k/128 * per_block] -> contiguous [.., k/128, n, per_block]"""
+    t = t.unflatten(-1, (-1, per_block))
+    return t.transpose(-3, -2).contiguous()
+
+
+def _pack_nibbles(q: torch.Tensor) -> torch.Tensor:
+    q = q.unflatten(-1, (-1, 2))
+    return (q[..., 0] | (q[..., 1] << 4)).contiguous()
+
+
+def int4_weight(q: torch.Tensor, scale: torch.Tensor, zero: torch.Tensor | None = None) -> Weight:
+    """Lays out an int4 weight: codes q uint8 [(experts,) n, k] in 0..15, scale [.., n, k/group] (rounded to
+    bf16) and, optionally, integer zero points of scale's shape; value = (q - zero) * scale, zero = 8 if absent."""
+    if q.dtype != torch.uint8 or q.dim() not in (2, 3) or q.shape[-1] % 128 or not q.numel():
+        raise ValueError("q must be uint8 [(experts,) n, k] with k a multiple of 128")
+    if scale.shape[:-1] != q.shape[:-1] or (zero is not None and zero.shape != scale.shape):
+        raise ValueError("scale (and zero) must be [(experts,) n, k/group]")
+    n, k = q.shape[-2:]
+    group = k // max(scale.shape[-1], 1)
+    if group not in (32, 64, 128) or scale.shape[-1] * group != k:
+        raise ValueError("scale must have k/32, k/64 or k/128 columns")
+    if int(q.max()) > 15 or (zero is not None and not 0 <= int(zero.min()) <= int(zero.max()) <= 15):
+        raise ValueError("codes and zero points must be in 0..15")
+    # k = 32 s + 8 g + 2 h + b of a block is nibble 4 b + h of word 4 g + s
+    w = q.unflatten(-1, (k // 128, 4, 4, 4, 2))
+    lead = w.dim() - 4
+    w = w.permute(*range(lead), lead + 1, lead, lead + 3, lead + 2).reshape(*q.shape)
+    return Weight("int4", n, k, _pack_nibbles(w), _blocks_first(scale.to(torch.bfloat16), 128 // group),
+                  zero=None if zero is None else _blocks_first(zero.to(torch.uint8), 128 // group), group=group,
+                  experts=q.shape[0] if q.dim() == 3 else 1)
+
+
+def e2m1_weight(codes: torch.Tensor, e8m0: torch.Tensor) -> Weight:
+    """Lays out an e2m1 weight: codes uint8 [(experts,) n, k] in 0..15 and the e8m0 codes uint8 [.., n, k/32]."""
+    if codes.dtype != torch.uint8 or codes.dim() not in (2, 3) or codes.shape[-1] % 128 or not codes.numel():
+        raise ValueError("codes must be uint8 [(experts,) n, k] with k a multiple of 128")
+    n, k = codes.shape[-2:]
+    if e8m0.dtype != torch.uint8 or e8m0.shape != (*codes.shape[:-1], k // 32):
+        raise ValueError("e8m0 must be uint8 [(experts,) n, k/32]")
+    if int(codes.max()) > 15:
+        raise ValueError("codes must be in 0..15")
+    packed = _blocks_first(e8m0, 4).view(torch.int32).squeeze(-1)
+    return Weight("e2m1_mx", n, k, _pack_nibbles(codes), packed, experts=codes.shape[0] if codes.dim() == 3 else 1)
+
+
+def _same_device(*named) -> torch.device:
+    """The one device of the tensors, which has to be a GPU."""
+    device = named[0][1].device
+    if device.type != "cuda":
+        raise ValueError(f"{named[0][0]} must be a device tensor")
+    for name, t in named[1:]:
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, {named[0][0]} on {device}")
+    return device
+
+
+def _dtype(t: torch.Tensor, name: str, dtypes) -> None:
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {dtypes}, got {t.dtype}")
+
+
+def _rows(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
+    """Row stride (elements) of a [rows, cols] tensor whose rows are contiguous."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return max(t.stride(0), cols) if rows <= 1 else t.stride(0)
+
+
+def _launch(device: torch.device, fn: str, *args) -> None:
+    """Calls fn(*args, stream) with `device` current, on its current stream."""
+    if device.index == torch.cuda.current_device():
+        _check(fn, getattr(lib(), fn)(*args, torch.cuda.current_stream(device).cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(fn, getattr(lib(), fn)(*args, torch.cuda.current_stream(device).cuda_stream))
+
+
+def moe_route_topk(d: Dims, logits, renormalise: bool, scale: float, topk_ids, topk_w) -> None:
+    device = _same_device(("logits", logits), ("topk_ids", topk_ids), ("topk_w", topk_w))
+    _dtype(logits, "logits", (torch.float32, torch.bfloat16))
+    _dtype(topk_w, "topk_w", (torch.float32,))
+    stride = _rows(logits, "logits", d.T, d.E)
+    _launch(device, "moe_route_topk", ctypes.byref(d.c()), logits.data_ptr(), int(logits.dtype == torch.bfloat16),
+            stride, int(bool(renormalise)), float(scale), _i32(topk_ids, "topk_ids", d.T * d.k),
+            _ptr(topk_w, "topk_w", 4 * d.T * d.k))
+
+
+def moe_matvec(x_bf16, weight: Weight, y_bf16) -> None:
+    device = _same_device(("x_bf16", x_bf16), ("weight", weight), ("y_bf16", y_bf16))
+    _dtype(x_bf16, "x_bf16", _BF16_BITS)
+    _dtype(y_bf16, "y_bf16", _BF16_BITS)
+    if weight.experts != 1:
+        raise ValueError(f"weight must be one matrix, got {weight.experts}")
+    m = x_bf16.shape[0]
+    xs, ys = _rows(x_bf16, "x_bf16", m, weight.k), _rows(y_bf16, "y_bf16", m, weight.n)
+    _launch(device, "moe_matvec", m, weight.n, weight.k, x_bf16.data_ptr(), xs, weight.c(), y_bf16.data_ptr(), ys)
+
+
+def moe_few_token_layer_workspace(d: Dims, inter: int) -> int:
+    b = ctypes.c_size_t()
+    _check("moe_few_token_layer_workspace",
+           lib().moe_few_token_layer_workspace(ctypes.byref(d.c()), inter, ctypes.byref(b)))
+    return b.value
+
+
+def moe_few_token_layer(d: Dims, inter: int, x_bf16, topk_ids, topk_w, w1: Weight, w2: Weight, out_bf16, ws) -> None:
+    device = _same_device(("x_bf16", x_bf16), ("topk_ids", topk_ids), ("topk_w", topk_w), ("w1", w1), ("w2", w2),
+                          ("out_bf16", out_bf16), ("ws", ws))
+    _dtype(x_bf16, "x_bf16", _BF16_BITS)
+    _dtype(topk_w, "topk_w", (torch.float32,))
+    _dtype(out_bf16, "out_bf16", _BF16_BITS)
+    for name, w, shape in (("w1", w1, (d.L, 2 * inter, d.H)), ("w2", w2, (d.L, d.H, inter))):
+        if (w.experts, w.n, w.k) != shape:
+            raise ValueError(f"{name} must be {shape[0]} matrices of [{shape[1]}, {shape[2]}], got {w.experts} of "
+                             f"[{w.n}, {w.k}]")
+    T = d.T
+    _launch(device, "moe_few_token_layer", ctypes.byref(d.c()), inter, _ptr(x_bf16, "x_bf16", 2 * T * d.H),
+            _i32(topk_ids, "topk_ids", T * d.k), _ptr(topk_w, "topk_w", 4 * T * d.k), w1.c(), w2.c(),
+            _ptr(out_bf16, "out_bf16", 2 * T * d.H), _ptr(ws, "ws"), ws.numel() * ws.element_size())
+
+
+def route_topk(d: Dims, logits, renormalise: bool = True, scale: float = 1.0, topk_ids=None, topk_w=None):
+    """logits [T, E] (float32 or bfloat16) -> (topk_ids int32 [T, k], topk_w float32 [T, k])"""
+    topk_ids = (torch.empty((d.T, d.k), dtype=torch.int32, device=logits.device) if topk_ids is None else topk_ids)
+    topk_w = torch.empty((d.T, d.k), dtype=torch.float32, device=logits.device) if topk_w is None else topk_w
+    moe_route_topk(d, logits, renormalise, scale, topk_ids, topk_w)
+    return topk_ids, topk_w
+
+
+def matvec(x, weight: Weight, out=None):
+    """x bf16 [m, k] times a weight [n, k], transposed -> bf16 [m, n]"""
+    out = torch.empty((x.shape[0], weight.n), dtype=torch.bfloat16, device=x.device) if out is None else out
+    moe_matvec(x, weight, out)
+    return out
+
+
+def alloc_few_token_workspace(d: Dims, inter: int, device="cuda") -> torch.Tensor:
+    return torch.empty(max(moe_few_token_layer_workspace(d, inter), 16), dtype=torch.uint8, device=device)
+
+
+def few_token_layer(d: Dims, inter: int, x, topk_ids, topk_w, w1: Weight, w2: Weight, out=None, ws=None):
+    """The expert layer on x bf16 [T, H] -> bf16 [T, H]: w1 the L gate-and-up matrices, w2 the down matrices."""
+    out = torch.empty((d.T, d.H), dtype=torch.bfloat16, device=x.device) if out is None else out
+    ws = alloc_few_token_workspace(d, inter, x.device) if ws is None else ws
+    moe_few_token_layer(d, inter, x, topk_ids, topk_w, w1, w2, out, ws)
     return out

@@ -18,7 +18,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoe_hotpath.so")
-SOURCES = ["api.hip", "layout.hip", "quant.hip", "gemm1.hip", "stage2.hip", "combine.hip"]
+SOURCES = ["api.hip", "layout.hip", "quant.hip", "gemm1.hip", "stage2.hip", "combine.hip",
+           "route_topk.hip", "few_token.hip"]
 TRACE_LIB = os.path.join(PKG, "libmoe_hotpath_trace.so")
 CEILING_LIB = os.path.join(PKG, "libmoe_ceiling.so")
 CEILING_SOURCES = ["ceiling.hip"]

@@ -1,0 +1,455 @@
+// The serving forms for a few tokens: the matrix-vector products over block-scaled weights (moe_matvec) and the
+// whole expert layer in two launches (moe_few_token_layer).  Both stream the weights once through the loop of
+// weight_stream.h; everything else (tokens, ids, intermediate rows) stays in cache.
+#include "weight_stream.h"
+
+namespace {
+
+using namespace moe;
+
+constexpr int kWaves = 8;                  // wavefronts of a workgroup; they split the K blocks
+constexpr int kThreads = kWaves * MOE_WAVE;
+constexpr int depth_of(int CT) { return CT == 1 ? 4 : CT == 2 ? 2 : 1; }   // K blocks a wavefront keeps in flight
+constexpr int kChunk = 64;                 // tokens a layer launch handles: one lane each, four column tiles
+constexpr int kMaxTopK = 64;
+constexpr int kMaxLocal = 1024;
+
+__device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane(threadIdx.x / MOE_WAVE); }
+
+// Sums the wavefronts' partial tiles (fixed order): element at (r * CT + c, lane).
+template <int N>
+__device__ __forceinline__ f32x4 sum_waves(const f32x4 (&red)[kWaves][N], int at) {
+    f32x4 s = red[0][at];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) s += red[w][at];
+    return s;
+}
+
+__device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
+    *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+}
+
+// acc += blocks [0, n) that load(step) brings, depth_of(CT) of them in flight; load returns block_product's cols.
+template <int FMT, int G, int R, int CT, class Load>
+__device__ __forceinline__ void stream_blocks(int n, Load&& load, f32x4 (&acc)[R][CT]) {
+    constexpr int kDepth = depth_of(CT);
+    Step<FMT, G, R, CT> st[kDepth];
+    uint32_t cols[kDepth];
+#pragma unroll
+    for (int u = 0; u < kDepth; ++u)
+        if (u < n) cols[u] = load(st[u]);
+    for (int i = 0; i < n; i += kDepth) {
+#pragma unroll
+        for (int u = 0; u < kDepth; ++u) {
+            if (i + u < n) {
+                block_product<FMT, G, R, CT>(st[u], cols[u], acc);
+                if (i + u + kDepth < n) cols[u] = load(st[u]);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- y = x W^T
+template <int FMT, int G, int R, int CT>
+__global__ void __launch_bounds__(kThreads)
+matvec_kernel(WView w, const uint16_t* __restrict__ x, int64_t ldx, int M, uint16_t* __restrict__ y, int64_t ldy) {
+    __shared__ f32x4 red[kWaves][R * CT * 64];
+    const int lane = lane_id(), wave = wave_index(), g = lane >> 4;
+    const int64_t row0 = (int64_t)blockIdx.x * (16 * R);
+    const int64_t col0 = (int64_t)blockIdx.y * (16 * CT);
+    const int ncols = (int)min<int64_t>(M - col0, 16 * CT);
+
+    TileRows<FMT, G> rows[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r)              // rows past n repeat the last ones and are not stored
+        rows[r] = tile_rows<FMT, G>(w, min(row0 + 16 * r + (lane & 15), w.n - 1), min(row0 + 16 * r + 4 * g, w.n - 4));
+    const __amdgpu_buffer_rsrc_t xb =
+        row_buffer(x + col0 * ldx, (uint32_t)(((int64_t)(ncols - 1) * ldx + (int64_t)w.nb * kKBlock) * 2));
+    uint32_t xrow[CT];
+    uint32_t cols = 0;
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+        const int t = 16 * c + (lane & 15);
+        xrow[c] = t < ncols ? (uint32_t)(t * ldx * 2) : kNoRow;
+        if (16 * c < ncols) cols |= 1u << c;
+    }
+
+    f32x4 acc[R][CT] = {};
+    int kb = w.nb * wave / kWaves;
+    const int n = w.nb * (wave + 1) / kWaves - kb;
+    stream_blocks<FMT, G, R, CT>(n, [&](Step<FMT, G, R, CT>& st) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) load_weights<FMT, G>(rows[r], w, kb, st.w[r], st.s[r]);
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+            if (CT == 1 || (cols >> c & 1)) load_rows<FMT, G>(xb, xrow[c], kb, st.x[c]);
+        ++kb;
+        return cols;
+    }, acc);
+
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) red[wave][(r * CT + c) * 64 + lane] = acc[r][c];
+    __syncthreads();
+    for (int at = threadIdx.x; at < R * CT * 64; at += kThreads) {
+        const int r = at / (64 * CT), c = at / 64 % CT, l = at & 63;
+        const int64_t row = row0 + 16 * r + 4 * (l >> 4);
+        const int t = 16 * c + (l & 15);
+        if (t < ncols && row < w.n) store4(y + (col0 + t) * ldy + row, sum_waves(red, at));
+    }
+}
+
+// ---------------------------------------------------------------- the layer
+struct LayerArgs {
+    const uint16_t* x;           // [T, H]
+    const int32_t* ids;          // [T, k]
+    const float* topk_w;         // [T, k]
+    uint16_t* h;                 // [T * k, I], the workspace
+    uint16_t* out;               // [T, H]
+    int T, k, e0, L, H, I;       // T <= kChunk
+};
+
+// The set of local experts that the tokens name, as bits in LDS (every thread calls; ends in a barrier).
+__device__ __forceinline__ void expert_set(const LayerArgs& a, uint32_t (&bits)[kMaxLocal / 32]) {
+    if (threadIdx.x < kMaxLocal / 32) bits[threadIdx.x] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.T * a.k; i += kThreads) {
+        const int64_t e = (int64_t)a.ids[i] - a.e0;
+        if (e >= 0 && e < a.L) atomicOr(&bits[e >> 5], 1u << (e & 31));
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ int expert_count(const uint32_t (&bits)[kMaxLocal / 32]) {
+    const int l = lane_id();
+    return __builtin_amdgcn_readfirstlane(wave_sum(l < kMaxLocal / 32 ? __popc(bits[l]) : 0));
+}
+
+// The n-th expert of the set (n < expert_count), uniform.
+__device__ __forceinline__ int nth_expert(const uint32_t (&bits)[kMaxLocal / 32], int n) {
+    const int l = lane_id();
+    const uint32_t mine = l < kMaxLocal / 32 ? bits[l] : 0;
+    const int upto = wave_inclusive_scan(__popc(mine));
+    const int word = __ffsll((unsigned long long)__ballot(upto > n)) - 1;
+    uint32_t b = (uint32_t)__builtin_amdgcn_readlane((int)mine, word);
+    int skip = n - (__builtin_amdgcn_readlane(upto, word) - __popc(b));
+    for (; skip > 0; --skip) b &= b - 1;
+    return word * 32 + __ffs(b) - 1;
+}
+
+__device__ __forceinline__ int next_expert(const uint32_t (&bits)[kMaxLocal / 32], int e) {
+    int word = e >> 5;
+    uint32_t b = __builtin_amdgcn_readfirstlane(bits[word]) & ~((2u << (e & 31)) - 1u);
+    while (b == 0 && ++word < kMaxLocal / 32) b = __builtin_amdgcn_readfirstlane(bits[word]);
+    return b ? word * 32 + __ffs(b) - 1 : -1;
+}
+
+template <int FMT, int G>
+__device__ __forceinline__ WView expert_view(const WView& w, int e) {
+    using F = Fmt<FMT, G>;
+    WView v = w;
+    v.data += (int64_t)e * w.n * w.nb * F::kRowBytes;
+    const int64_t blocks = (int64_t)e * w.n * w.nb;
+    if constexpr (F::kInt4) {
+        v.scale = static_cast<const uint8_t*>(w.scale) + blocks * 2 * G;
+        if (w.zero) v.zero = w.zero + blocks * G;
+    } else if constexpr (F::kMx) {
+        v.scale = static_cast<const uint8_t*>(w.scale) + blocks * 4;
+    } else {
+        v.scale = static_cast<const uint8_t*>(w.scale) + blocks / 128 * 4;
+    }
+    return v;
+}
+
+// First launch: h[t k + j] = w (silu(gate) up) in bf16, for the first slot j in which token t names the expert, w
+// the sum of the token's weights for it.  A workgroup takes 8 R columns of h of one expert: a tile's sixteen weight
+// rows are eight gate rows and the eight up rows that go with them.  The rounding of h to bf16 is the matrix
+// instruction's input type; it is of the size of the output's own.
+template <int FMT, int G, int R, int CT>
+__global__ void __launch_bounds__(kThreads)
+gate_up_kernel(WView w, LayerArgs a) {
+    __shared__ f32x4 red[kWaves][R * CT * 64];
+    __shared__ uint32_t bits[kMaxLocal / 32];
+    __shared__ int32_t tok[kChunk], slot[kChunk];
+    __shared__ float wt[kChunk];
+    expert_set(a, bits);
+    if ((int)blockIdx.y >= expert_count(bits)) return;
+    const int e = nth_expert(bits, blockIdx.y);
+    const int lane = lane_id(), wave = wave_index(), g = lane >> 4;
+
+    int first = -1;                          // lane t: the slot of token t
+    float sum = 0.f;
+    if (lane < a.T)
+        for (int j = a.k - 1; j >= 0; --j)
+            if (a.ids[lane * a.k + j] == a.e0 + e) first = j;
+    if (first >= 0)
+        for (int j = first; j < a.k; ++j)
+            if (a.ids[lane * a.k + j] == a.e0 + e) sum += a.topk_w[lane * a.k + j];
+    const uint64_t here = __ballot(first >= 0);
+    const int ncols = __popcll(here);
+    if (wave == 0 && first >= 0) {
+        const int at = __popcll(here & lanemask_lt());
+        tok[at] = lane, slot[at] = lane * a.k + first, wt[at] = sum;
+    }
+    __syncthreads();
+
+    const WView v = expert_view<FMT, G>(w, e);
+    const int i0 = blockIdx.x * (8 * R);
+    TileRows<FMT, G> rows[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int ar = lane & 15, dr = 4 * g;
+        rows[r] = tile_rows<FMT, G>(v, (ar < 8 ? 0 : a.I - 8) + i0 + 8 * r + ar,
+                                    (dr < 8 ? 0 : a.I - 8) + i0 + 8 * r + dr);
+    }
+    const __amdgpu_buffer_rsrc_t xb = row_buffer(a.x, (uint32_t)(a.T * a.H * 2));
+    uint32_t xrow[CT];
+    uint32_t cols = 0;
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+        const int t = 16 * c + (lane & 15);
+        xrow[c] = t < ncols ? (uint32_t)(tok[t] * a.H * 2) : kNoRow;
+        if (16 * c < ncols) cols |= 1u << c;
+    }
+
+    f32x4 acc[R][CT] = {};
+    int kb = v.nb * wave / kWaves;
+    const int n = v.nb * (wave + 1) / kWaves - kb;
+    stream_blocks<FMT, G, R, CT>(n, [&](Step<FMT, G, R, CT>& st) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) load_weights<FMT, G>(rows[r], v, kb, st.w[r], st.s[r]);
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+            if (CT == 1 || (cols >> c & 1)) load_rows<FMT, G>(xb, xrow[c], kb, st.x[c]);
+        ++kb;
+        return cols;
+    }, acc);
+
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) red[wave][(r * CT + c) * 64 + lane] = acc[r][c];
+    __syncthreads();
+    for (int at = threadIdx.x; at < R * CT * 32; at += kThreads) {
+        const int r = at / (32 * CT), c = at / 32 % CT, l = at & 31;     // lanes 0..31 hold gate rows, 32..63 up rows
+        const int t = 16 * c + (l & 15);
+        if (t >= ncols) continue;
+        const f32x4 gate = sum_waves(red, (r * CT + c) * 64 + l);
+        const f32x4 up = sum_waves(red, (r * CT + c) * 64 + l + 32);
+        f32x4 h;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = gate[i] / (1.0f + __expf(-gate[i])) * up[i] * wt[t];
+        store4(a.h + (int64_t)slot[t] * a.I + i0 + 8 * r + 4 * (l >> 4), h);
+    }
+}
+
+// Second launch: out[t] = sum over the experts of W2[e] h[t, e], one long product whose K runs over the experts
+// hit.  The sixteen columns are the tokens themselves (a token that does not name the expert reads zeros), so the
+// sum over experts stays in the accumulators and its order is fixed.
+template <int FMT, int G, int R, int CT>
+__global__ void __launch_bounds__(kThreads)
+down_kernel(WView w, LayerArgs a) {
+    __shared__ f32x4 red[kWaves][R * CT * 64];
+    __shared__ uint32_t bits[kMaxLocal / 32];
+    extern __shared__ int32_t ids[];         // [T * k]
+    for (int i = threadIdx.x; i < a.T * a.k; i += kThreads) ids[i] = a.ids[i];
+    expert_set(a, bits);
+    const int lane = lane_id(), wave = wave_index(), g = lane >> 4;
+    const int row0 = blockIdx.x * (16 * R);
+    const int64_t total = (int64_t)expert_count(bits) * w.nb;
+    const int64_t f0 = total * wave / kWaves;
+    const int n = (int)(total * (wave + 1) / kWaves - f0);
+
+    const __amdgpu_buffer_rsrc_t hb = row_buffer(a.h, (uint32_t)(a.T * a.k * a.I * 2));
+    int e = 0, kb = 0;
+    WView v = w;
+    TileRows<FMT, G> rows[R];
+    uint32_t hrow[CT];
+    uint32_t cols = 0;
+    auto enter = [&](int expert) {           // this lane's rows and columns of an expert
+        e = expert;
+        v = expert_view<FMT, G>(w, e);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            rows[r] = tile_rows<FMT, G>(v, row0 + 16 * r + (lane & 15), row0 + 16 * r + 4 * g);
+        cols = 0;
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+            const int t = 16 * c + (lane & 15);
+            hrow[c] = kNoRow;
+            if (t < a.T)
+                for (int j = a.k - 1; j >= 0; --j)
+                    if (ids[t * a.k + j] == a.e0 + e) hrow[c] = (uint32_t)((t * a.k + j) * a.I * 2);
+            if (__ballot(hrow[c] != kNoRow)) cols |= 1u << c;
+        }
+    };
+    if (n > 0) {
+        kb = (int)(f0 % w.nb);
+        enter(nth_expert(bits, (int)(f0 / w.nb)));
+    }
+    f32x4 acc[R][CT] = {};
+    stream_blocks<FMT, G, R, CT>(n, [&](Step<FMT, G, R, CT>& st) {
+        if (kb == w.nb) {
+            kb = 0;
+            enter(next_expert(bits, e));
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) load_weights<FMT, G>(rows[r], v, kb, st.w[r], st.s[r]);
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+            if (CT == 1 || (cols >> c & 1)) load_rows<FMT, G>(hb, hrow[c], kb, st.x[c]);
+        ++kb;
+        return cols;
+    }, acc);
+
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) red[wave][(r * CT + c) * 64 + lane] = acc[r][c];
+    __syncthreads();
+    for (int at = threadIdx.x; at < R * CT * 64; at += kThreads) {
+        const int r = at / (64 * CT), c = at / 64 % CT, l = at & 63;
+        const int t = 16 * c + (l & 15);
+        if (t < a.T) store4(a.out + (int64_t)t * a.H + row0 + 16 * r + 4 * (l >> 4), sum_waves(red, at));
+    }
+}
+
+// ---------------------------------------------------------------- host side
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+// A weight descriptor for an [n, k] matrix (per expert), checked; groups = scale groups per K block for int4.
+moe_status load_weight(const moe_weight* w, int64_t n, int64_t k, WView* v, int* groups) {
+    if (!w || n < 4 || n % 4 != 0 || k < kKBlock || k % kKBlock != 0) return MOE_ERR_INVALID_ARG;
+    *groups = 1;
+    switch (w->format) {
+        case MOE_W_E4M3:
+            if (n % 128 != 0) return MOE_ERR_INVALID_ARG;
+            break;
+        case MOE_W_E4M3_MX:
+        case MOE_W_E2M1_MX: break;
+        case MOE_W_INT4:
+            if (w->group != 32 && w->group != 64 && w->group != 128) return MOE_ERR_INVALID_ARG;
+            *groups = kKBlock / w->group;
+            break;
+        default: return MOE_ERR_INVALID_ARG;
+    }
+    if (w->format != MOE_W_INT4 && w->zero) return MOE_ERR_INVALID_ARG;
+    if (!w->data || !w->scale) return MOE_ERR_INVALID_ARG;
+    if (!aligned(w->data, 16) || !aligned(w->scale, 16) || !aligned(w->zero, 16)) return MOE_ERR_INVALID_ARG;
+    v->data = static_cast<const uint8_t*>(w->data);
+    v->scale = w->scale;
+    v->zero = w->zero;
+    v->n = n;
+    v->nb = (int)(k / kKBlock);
+    return MOE_OK;
+}
+
+template <class F>
+moe_status with_format(int format, int groups, F&& f) {
+    switch (format) {
+        case MOE_W_E4M3: return f(std::integral_constant<int, MOE_W_E4M3>{}, std::integral_constant<int, 1>{});
+        case MOE_W_E4M3_MX: return f(std::integral_constant<int, MOE_W_E4M3_MX>{}, std::integral_constant<int, 1>{});
+        case MOE_W_E2M1_MX: return f(std::integral_constant<int, MOE_W_E2M1_MX>{}, std::integral_constant<int, 1>{});
+        default: break;
+    }
+    if (groups == 1) return f(std::integral_constant<int, MOE_W_INT4>{}, std::integral_constant<int, 1>{});
+    if (groups == 2) return f(std::integral_constant<int, MOE_W_INT4>{}, std::integral_constant<int, 2>{});
+    return f(std::integral_constant<int, MOE_W_INT4>{}, std::integral_constant<int, 4>{});
+}
+
+// Column tiles a launch covers: 1, 2 or 4.
+template <class F>
+void with_cols(int64_t tokens, F&& f) {
+    if (tokens <= 16) f(std::integral_constant<int, 1>{});
+    else if (tokens <= 32) f(std::integral_constant<int, 2>{});
+    else f(std::integral_constant<int, 4>{});
+}
+
+}  // namespace
+
+extern "C" moe_status moe_matvec(int32_t m, int32_t n, int32_t k, const uint16_t* x_bf16, int64_t x_stride,
+                                 const moe_weight* w, uint16_t* y_bf16, int64_t y_stride, void* hip_stream) {
+    if (m < 0) return MOE_ERR_INVALID_ARG;
+    WView v;
+    int groups;
+    moe_status st = load_weight(w, n, k, &v, &groups);
+    if (st != MOE_OK) return st;
+    if (m == 0) return MOE_OK;
+    if (!x_bf16 || !y_bf16 || !aligned(x_bf16, 16) || !aligned(y_bf16, 8)) return MOE_ERR_INVALID_ARG;
+    if (x_stride < k || x_stride % 8 != 0 || y_stride < n || y_stride % 4 != 0) return MOE_ERR_INVALID_ARG;
+    // a workgroup's token rows are addressed with 31-bit byte offsets
+    if (x_stride >= (1 << 24)) return MOE_ERR_UNSUPPORTED;
+    hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
+    return with_format(w->format, groups, [&](auto fmt, auto g) {
+        with_cols(m, [&](auto ct) {
+            constexpr int R = 1;
+            const dim3 grid((unsigned)((n + 16 * R - 1) / (16 * R)), (unsigned)((m + 16 * ct - 1) / (16 * ct)));
+            matvec_kernel<fmt, g, R, ct><<<grid, kThreads, 0, stream>>>(v, x_bf16, x_stride, m, y_bf16, y_stride);
+        });
+        return launch_status();
+    });
+}
+
+extern "C" moe_status moe_few_token_layer_workspace(const moe_dims* dims, int32_t inter, size_t* bytes) {
+    Dims d;
+    moe_status st = load_dims(dims, &d, true);
+    if (st != MOE_OK) return st;
+    if (!bytes || inter < 128 || inter % 128 != 0) return MOE_ERR_INVALID_ARG;
+    if (d.L > kMaxLocal || d.k > kMaxTopK) return MOE_ERR_UNSUPPORTED;
+    *bytes = (size_t)(std::min<int64_t>(d.T, kChunk) * d.k * inter * 2 + 255) / 256 * 256;
+    return MOE_OK;
+}
+
+extern "C" moe_status moe_few_token_layer(const moe_dims* dims, int32_t inter, const uint16_t* x_bf16,
+                                          const int32_t* topk_ids, const float* topk_w, const moe_weight* w1,
+                                          const moe_weight* w2, uint16_t* out_bf16, void* ws, size_t ws_bytes,
+                                          void* hip_stream) {
+    size_t need;
+    moe_status st = moe_few_token_layer_workspace(dims, inter, &need);
+    if (st != MOE_OK) return st;
+    Dims d;
+    st = load_dims(dims, &d, true);
+    if (st != MOE_OK) return st;
+    WView v1, v2;
+    int g1, g2;
+    st = load_weight(w1, 2 * (int64_t)inter, d.H, &v1, &g1);
+    if (st != MOE_OK) return st;
+    st = load_weight(w2, d.H, inter, &v2, &g2);
+    if (st != MOE_OK) return st;
+    if (d.T == 0) return MOE_OK;
+    if (!x_bf16 || !topk_ids || !topk_w || !out_bf16) return MOE_ERR_INVALID_ARG;
+    if (!aligned(x_bf16, 16) || !aligned(out_bf16, 8)) return MOE_ERR_INVALID_ARG;
+    // token and intermediate rows are addressed with 31-bit byte offsets
+    const int64_t chunk = std::min<int64_t>(d.T, kChunk);
+    if (chunk * d.H * 2 > INT32_MAX || chunk * d.k * inter * 2 > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    if (!ws || ws_bytes < need || !aligned(ws, 16)) return MOE_ERR_WORKSPACE;
+    hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
+    for (int64_t t0 = 0; t0 < d.T && st == MOE_OK; t0 += kChunk) {
+        LayerArgs a;
+        a.x = x_bf16 + t0 * d.H;
+        a.ids = topk_ids + t0 * d.k;
+        a.topk_w = topk_w + t0 * d.k;
+        a.h = static_cast<uint16_t*>(ws);
+        a.out = out_bf16 + t0 * d.H;
+        a.T = (int)std::min<int64_t>(d.T - t0, kChunk);
+        a.k = (int)d.k, a.e0 = (int)d.e0, a.L = (int)d.L, a.H = (int)d.H, a.I = inter;
+        st = with_format(w1->format, g1, [&](auto fmt, auto g) {
+            with_cols(a.T, [&](auto ct) {
+                constexpr int R = 1;
+                const dim3 grid((unsigned)(inter / (8 * R)), (unsigned)std::min<int64_t>(a.T * d.k, d.L));
+                gate_up_kernel<fmt, g, R, ct><<<grid, kThreads, 0, stream>>>(v1, a);
+            });
+            return launch_status();
+        });
+        if (st != MOE_OK) return st;
+        st = with_format(w2->format, g2, [&](auto fmt, auto g) {
+            with_cols(a.T, [&](auto ct) {
+                constexpr int R = 1;
+                down_kernel<fmt, g, R, ct><<<dim3((unsigned)(d.H / (16 * R))), kThreads, a.T * a.k * 4, stream>>>(v2, a);
+            });
+            return launch_status();
+        });
+    }
+    return st;
+}

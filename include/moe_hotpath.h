@@ -346,6 +346,105 @@ moe_status moe_combine(const moe_dims* dims, int32_t width, const uint16_t* y_bf
                        int64_t y_rows, const int32_t* assign_row, const float* topk_w,
                        uint16_t* out_bf16, void* hip_stream);
 
+/*
+ * Serving forms for a few tokens: the router's choice, the matrix-vector
+ * products over block-scaled weights, and the whole expert layer in two
+ * launches.  A batch of decoded tokens reads every expert it hits once and
+ * computes almost nothing with it, so these calls keep the tokens in bf16 and
+ * widen the weights on the way from memory; the staged calls above are the
+ * form for batches that fill their 128-row tiles.
+ *
+ * moe_route_topk: for each token t < T, the k experts with the largest logits,
+ * larger first, ties to the lower id (an exact choice, made on the logits):
+ *   renormalise != 0:  w[t, j] = scale * exp(l_j - l_0) / sum over the chosen
+ *   renormalise == 0:  w[t, j] = scale * exp(l_j - l_0) / sum over all experts
+ * with l_0 the largest and the sums in fp32.  A logit of -inf (an expert
+ * masked off) or NaN is never chosen and adds nothing; a row that offers fewer
+ * than k experts gets id -1 and weight 0 in the slots left over, which the
+ * layout and the few-token layer skip.  Logits of +inf share the whole weight.
+ * In:  logits float32 (logits_bf16 == 0) or bf16 bits (logits_bf16 != 0), row
+ *      t at logits + t * logits_stride elements, logits_stride >= E.
+ * Out: topk_ids int32 [T, k] (global expert ids);  topk_w float32 [T, k].
+ * Uses T, k and E of dims.  E <= 1024 and k <= 64, else MOE_ERR_UNSUPPORTED.
+ */
+moe_status moe_route_topk(const moe_dims* dims, const void* logits, int32_t logits_bf16,
+                          int64_t logits_stride, int32_t renormalise, float scale,
+                          int32_t* topk_ids, float* topk_w, void* hip_stream);
+
+/*
+ * A weight matrix [n, k] (output rows, K-contiguous), or L of them one after
+ * the other, in one of four formats.  k is a multiple of 128 (the K block).
+ *   MOE_W_E4M3     data uint8 [L, n, k] e4m3; scale float32 [L, n/128, k/128]:
+ *                  moe_grouped_gemm1's weights.  n a multiple of 128.
+ *   MOE_W_E4M3_MX  data uint8 [L, n, k] e4m3; scale uint32 [L, k/128, n], the
+ *                  e8m0 codes of four groups of 32: moe_grouped_gemm1_mx's.
+ *   MOE_W_E2M1_MX  data uint8 [L, n, k/2], e2m1 codes (magnitudes 0, 0.5, 1,
+ *                  1.5, 2, 3, 4, 6 and a sign bit), element 2i in byte i's low
+ *                  four bits; scale as MOE_W_E4M3_MX.
+ *   MOE_W_INT4     data uint8 [L, n, k/2], value (q - zero) * scale, q in
+ *                  0..15.  Within a K block element 32s + 8g + j (s, g < 4,
+ *                  j < 8) is nibble j/2 + 4*(j%2) of the block's little-endian
+ *                  32-bit word 4g + s.  group = 32, 64 or 128 elements along k
+ *                  share a scale: bf16 [L, k/128, n, 128/group], and zero
+ *                  uint8 [L, k/128, n, 128/group] in 0..15, or NULL for 8.
+ * n is a multiple of 4.  data, scale and zero are 16-byte aligned.  group is
+ * read for MOE_W_INT4 only; zero must be NULL for the others.  The struct is
+ * read on the host during the call.
+ */
+typedef enum moe_weight_format {
+    MOE_W_E4M3 = 0,
+    MOE_W_E4M3_MX = 1,
+    MOE_W_E2M1_MX = 2,
+    MOE_W_INT4 = 3
+} moe_weight_format;
+
+typedef struct moe_weight {
+    int32_t format;             /* a moe_weight_format                         */
+    int32_t group;              /* MOE_W_INT4: 32, 64 or 128                   */
+    const void* data;           /* device pointers                             */
+    const void* scale;
+    const uint8_t* zero;        /* MOE_W_INT4 only; NULL: every zero point is 8 */
+} moe_weight;
+
+/*
+ * Matrix-vector products: for row i < m and column c < n,
+ *   y[i, c] = bf16( sum_j x[i, j] * w[c, j] )
+ * in fp32 from the bf16 x and the exact weight values.  Made for a few rows
+ * (the weights are read once per 64 rows); any m >= 0 is computed.
+ * In:  x_bf16 bf16 bits, row i at x_bf16 + i * x_stride elements, 16-byte
+ *      aligned, x_stride >= k and a multiple of 8 (below 2^24);
+ *      w one matrix [n, k].
+ * Out: y_bf16 bf16 bits, row i at y_bf16 + i * y_stride elements, 8-byte
+ *      aligned, y_stride >= n and a multiple of 4.  Elements between the rows
+ *      are not written.
+ */
+moe_status moe_matvec(int32_t m, int32_t n, int32_t k, const uint16_t* x_bf16, int64_t x_stride,
+                      const moe_weight* w, uint16_t* y_bf16, int64_t y_stride, void* hip_stream);
+
+/* Workspace bytes moe_few_token_layer needs (host-only): min(T, 64) * k rows
+ * of inter bf16 values, padded to 256 B. */
+moe_status moe_few_token_layer_workspace(const moe_dims* dims, int32_t inter, size_t* bytes);
+
+/*
+ * The expert layer for a few tokens, in two launches:
+ *   out[t] = bf16( sum_j topk_w[t, j] * W2[e] (silu(G[e] x_t) * (U[e] x_t)) ),
+ *   e = topk_ids[t, j] - e0, over the slots j with e in [0, L)
+ * (any other id, negative too, is skipped; a token without a local expert gets
+ * zeros).  G and U are rows [0, inter) and [inter, 2*inter) of W1[e].  Products
+ * and sums in fp32; the weighted intermediate row is rounded to bf16 once.
+ * In:  x_bf16 uint16 [T, H], 16-byte aligned;  topk_ids int32 [T, k];
+ *      topk_w float32 [T, k];  w1: L matrices [2*inter, H];  w2: L matrices
+ *      [H, inter];  the two may have different formats.
+ * Out: out_bf16 uint16 [T, H], 8-byte aligned.
+ * ws: at least moe_few_token_layer_workspace bytes, 16-byte aligned, no
+ * initialisation.  Tokens go through in batches of 64, each of which reads the
+ * experts that it hits once; inter is a multiple of 128, L <= 1024, k <= 64.
+ */
+moe_status moe_few_token_layer(const moe_dims* dims, int32_t inter, const uint16_t* x_bf16,
+                               const int32_t* topk_ids, const float* topk_w, const moe_weight* w1,
+                               const moe_weight* w2, uint16_t* out_bf16, void* ws, size_t ws_bytes,
+                               void* hip_stream);
+
 #ifdef __cplusplus
 }
 #endif

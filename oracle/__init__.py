@@ -29,6 +29,8 @@ Each function is the plain definition of one step, written from the pages:
   down-projection with each row's routing weight, and the combine of the
   weighted rows (MegaMoE PR, "What": stage1 feeds stage2 + combine; commit
   "recv_layout": the layout's per-row routing weights serve stage2).
+* ``few_token`` - the serving forms: the router's top-k, products with 8- and
+  4-bit block-scaled weights, the whole expert layer for a few tokens.
 * ``fp8`` / ``bf16`` - the OCP FP8 E4M3 encoding and bf16 rounding the steps
   rely on.
 
@@ -37,4 +39,4 @@ invariants (bijection, contiguity, stability, half-ulp round trip, identity
 experts), torch's independent fp8/bf16 casts, and exact special cases.
 Every function here has at least one such pin; none is "parity unpinned".
 """
-from . import bf16, fp8, layout, quant, gemm1, combine, mx, stage2  # noqa: F401
+from . import bf16, fp8, layout, quant, gemm1, combine, mx, stage2, few_token  # noqa: F401
