@@ -3,13 +3,17 @@
 // weight_stream.h; everything else (tokens, ids, intermediate rows) stays in cache.
 #include "weight_stream.h"
 
+#include <cmath>
+#include <type_traits>
+
 namespace {
 
 using namespace moe;
 
 constexpr int kWaves = 8;                  // wavefronts of a workgroup; they split the K blocks
 constexpr int kThreads = kWaves * MOE_WAVE;
-constexpr int depth_of(int CT) { return CT == 1 ? 4 : CT == 2 ? 2 : 1; }   // K blocks a wavefront keeps in flight
+// K blocks a wavefront keeps in flight
+constexpr int depth_of(int R, int CT) { return CT > 2 || R == 4 ? 1 : CT == 2 || R == 2 ? 2 : 4; }
 constexpr int kChunk = 64;                 // tokens a layer launch handles: one lane each, four column tiles
 constexpr int kMaxTopK = 64;
 constexpr int kMaxLocal = 1024;
@@ -29,11 +33,11 @@ __device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
     *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 
-// acc += blocks [0, n) that load(step) brings, depth_of(CT) of them in flight; load returns block_product's cols.
-template <int FMT, int G, int R, int CT, class Load>
-__device__ __forceinline__ void stream_blocks(int n, Load&& load, f32x4 (&acc)[R][CT]) {
-    constexpr int kDepth = depth_of(CT);
-    Step<FMT, G, R, CT> st[kDepth];
+// acc += blocks [0, n) that load(step) brings, depth_of(R, CT) of them in flight; load returns block_product's cols.
+template <int FMT, int G, int R, int CT, int XT, class Load>
+__device__ __forceinline__ void stream_blocks(int n, Load&& load, u32x4* corner, f32x4 (&acc)[R][CT]) {
+    constexpr int kDepth = depth_of(R, CT);
+    Step<FMT, G, R, CT, XT> st[kDepth];
     uint32_t cols[kDepth];
 #pragma unroll
     for (int u = 0; u < kDepth; ++u)
@@ -42,7 +46,7 @@ __device__ __forceinline__ void stream_blocks(int n, Load&& load, f32x4 (&acc)[R
 #pragma unroll
         for (int u = 0; u < kDepth; ++u) {
             if (i + u < n) {
-                block_product<FMT, G, R, CT>(st[u], cols[u], acc);
+                block_product<FMT, G, R, CT, XT>(st[u], cols[u], corner, acc);
                 if (i + u + kDepth < n) cols[u] = load(st[u]);
             }
         }
@@ -50,42 +54,42 @@ __device__ __forceinline__ void stream_blocks(int n, Load&& load, f32x4 (&acc)[R
 }
 
 // ---------------------------------------------------------------- y = x W^T
-template <int FMT, int G, int R, int CT>
+template <int FMT, int G, int R, int CT, int XT>
 __global__ void __launch_bounds__(kThreads)
 matvec_kernel(WView w, const uint16_t* __restrict__ x, int64_t ldx, int M, uint16_t* __restrict__ y, int64_t ldy) {
     __shared__ f32x4 red[kWaves][R * CT * 64];
-    const int lane = lane_id(), wave = wave_index(), g = lane >> 4;
+    __shared__ u32x4 corner[kWaves][kCorner];
+    const int lane = lane_id(), wave = wave_index();
     const int64_t row0 = (int64_t)blockIdx.x * (16 * R);
-    const int64_t col0 = (int64_t)blockIdx.y * (16 * CT);
-    const int ncols = (int)min<int64_t>(M - col0, 16 * CT);
+    const int64_t col0 = (int64_t)blockIdx.y * (XT * CT);
+    const int ncols = (int)min<int64_t>(M - col0, XT * CT);
 
-    TileRows<FMT, G> rows[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r)              // rows past n repeat the last ones and are not stored
-        rows[r] = tile_rows<FMT, G>(w, min(row0 + 16 * r + (lane & 15), w.n - 1), min(row0 + 16 * r + 4 * g, w.n - 4));
+    // rows past n repeat the last ones and are not stored
+    const Tiles<FMT, G, R> tiles = tiles_of<FMT, G, R>(
+        w, [&](int t, int i) { return min(row0 + 16 * t + i, w.n - 1); },
+        [&](int t, int i) { return min(row0 + 16 * t + 4 * i, w.n - 4); });
     const __amdgpu_buffer_rsrc_t xb =
         row_buffer(x + col0 * ldx, (uint32_t)(((int64_t)(ncols - 1) * ldx + (int64_t)w.nb * kKBlock) * 2));
     uint32_t xrow[CT];
     uint32_t cols = 0;
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
-        const int t = 16 * c + (lane & 15);
+        const int t = XT * c + token_of_lane<XT>();
         xrow[c] = t < ncols ? (uint32_t)(t * ldx * 2) : kNoRow;
-        if (16 * c < ncols) cols |= 1u << c;
+        if (XT * c < ncols) cols |= 1u << c;
     }
 
     f32x4 acc[R][CT] = {};
     int kb = w.nb * wave / kWaves;
     const int n = w.nb * (wave + 1) / kWaves - kb;
-    stream_blocks<FMT, G, R, CT>(n, [&](Step<FMT, G, R, CT>& st) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) load_weights<FMT, G>(rows[r], w, kb, st.w[r], st.s[r]);
+    stream_blocks<FMT, G, R, CT, XT>(n, [&](Step<FMT, G, R, CT, XT>& st) {
+        load_weights<FMT, G, R>(tiles, w, kb, st.w, st.s);
 #pragma unroll
         for (int c = 0; c < CT; ++c)
-            if (CT == 1 || (cols >> c & 1)) load_rows<FMT, G>(xb, xrow[c], kb, st.x[c]);
+            if (CT == 1 || (cols >> c & 1)) load_rows<FMT, G, XT>(xb, xrow[c], kb, st.x[c]);
         ++kb;
         return cols;
-    }, acc);
+    }, corner[wave], acc);
 
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -95,7 +99,8 @@ matvec_kernel(WView w, const uint16_t* __restrict__ x, int64_t ldx, int M, uint1
     for (int at = threadIdx.x; at < R * CT * 64; at += kThreads) {
         const int r = at / (64 * CT), c = at / 64 % CT, l = at & 63;
         const int64_t row = row0 + 16 * r + 4 * (l >> 4);
-        const int t = 16 * c + (l & 15);
+        const int t = XT * c + (l & 15) / (16 / XT);
+        if ((l & 15) % (16 / XT)) continue;              // a repeated column
         if (t < ncols && row < w.n) store4(y + (col0 + t) * ldy + row, sum_waves(red, at));
     }
 }
@@ -114,7 +119,7 @@ struct LayerArgs {
 __device__ __forceinline__ void expert_set(const LayerArgs& a, uint32_t (&bits)[kMaxLocal / 32]) {
     if (threadIdx.x < kMaxLocal / 32) bits[threadIdx.x] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < a.T * a.k; i += kThreads) {
+    for (int i = threadIdx.x; i < a.T * a.k; i += blockDim.x) {
         const int64_t e = (int64_t)a.ids[i] - a.e0;
         if (e >= 0 && e < a.L) atomicOr(&bits[e >> 5], 1u << (e & 31));
     }
@@ -166,17 +171,18 @@ __device__ __forceinline__ WView expert_view(const WView& w, int e) {
 // the sum of the token's weights for it.  A workgroup takes 8 R columns of h of one expert: a tile's sixteen weight
 // rows are eight gate rows and the eight up rows that go with them.  The rounding of h to bf16 is the matrix
 // instruction's input type; it is of the size of the output's own.
-template <int FMT, int G, int R, int CT>
+template <int FMT, int G, int R, int CT, int XT>
 __global__ void __launch_bounds__(kThreads)
 gate_up_kernel(WView w, LayerArgs a) {
     __shared__ f32x4 red[kWaves][R * CT * 64];
+    __shared__ u32x4 corner[kWaves][kCorner];
     __shared__ uint32_t bits[kMaxLocal / 32];
     __shared__ int32_t tok[kChunk], slot[kChunk];
     __shared__ float wt[kChunk];
     expert_set(a, bits);
     if ((int)blockIdx.y >= expert_count(bits)) return;
     const int e = nth_expert(bits, blockIdx.y);
-    const int lane = lane_id(), wave = wave_index(), g = lane >> 4;
+    const int lane = lane_id(), wave = wave_index();
 
     int first = -1;                          // lane t: the slot of token t
     float sum = 0.f;
@@ -196,87 +202,86 @@ gate_up_kernel(WView w, LayerArgs a) {
 
     const WView v = expert_view<FMT, G>(w, e);
     const int i0 = blockIdx.x * (8 * R);
-    TileRows<FMT, G> rows[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int ar = lane & 15, dr = 4 * g;
-        rows[r] = tile_rows<FMT, G>(v, (ar < 8 ? 0 : a.I - 8) + i0 + 8 * r + ar,
-                                    (dr < 8 ? 0 : a.I - 8) + i0 + 8 * r + dr);
-    }
+    const auto row_of = [&](int t, int i) { return (i < 8 ? 0 : a.I - 8) + i0 + 8 * t + i; };
+    const Tiles<FMT, G, R> tiles =
+        tiles_of<FMT, G, R>(v, row_of, [&](int t, int i) { return row_of(t, 4 * i); });
     const __amdgpu_buffer_rsrc_t xb = row_buffer(a.x, (uint32_t)(a.T * a.H * 2));
-    uint32_t xrow[CT];
-    uint32_t cols = 0;
+    // an expert with more tokens than the column tiles hold takes further passes over the weights
+    for (int col0 = 0; col0 < ncols; col0 += XT * CT) {
+        uint32_t xrow[CT];
+        uint32_t cols = 0;
 #pragma unroll
-    for (int c = 0; c < CT; ++c) {
-        const int t = 16 * c + (lane & 15);
-        xrow[c] = t < ncols ? (uint32_t)(tok[t] * a.H * 2) : kNoRow;
-        if (16 * c < ncols) cols |= 1u << c;
-    }
+        for (int c = 0; c < CT; ++c) {
+            const int t = col0 + XT * c + token_of_lane<XT>();
+            xrow[c] = t < ncols ? (uint32_t)(tok[t] * a.H * 2) : kNoRow;
+            if (col0 + XT * c < ncols) cols |= 1u << c;
+        }
 
-    f32x4 acc[R][CT] = {};
-    int kb = v.nb * wave / kWaves;
-    const int n = v.nb * (wave + 1) / kWaves - kb;
-    stream_blocks<FMT, G, R, CT>(n, [&](Step<FMT, G, R, CT>& st) {
+        f32x4 acc[R][CT] = {};
+        int kb = v.nb * wave / kWaves;
+        const int n = v.nb * (wave + 1) / kWaves - kb;
+        stream_blocks<FMT, G, R, CT, XT>(n, [&](Step<FMT, G, R, CT, XT>& st) {
+            load_weights<FMT, G, R>(tiles, v, kb, st.w, st.s);
 #pragma unroll
-        for (int r = 0; r < R; ++r) load_weights<FMT, G>(rows[r], v, kb, st.w[r], st.s[r]);
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-            if (CT == 1 || (cols >> c & 1)) load_rows<FMT, G>(xb, xrow[c], kb, st.x[c]);
-        ++kb;
-        return cols;
-    }, acc);
+            for (int c = 0; c < CT; ++c)
+                if (CT == 1 || (cols >> c & 1)) load_rows<FMT, G, XT>(xb, xrow[c], kb, st.x[c]);
+            ++kb;
+            return cols;
+        }, corner[wave], acc);
 
+        if (col0 > 0) __syncthreads();       // the sums of the pass before are read
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int c = 0; c < CT; ++c) red[wave][(r * CT + c) * 64 + lane] = acc[r][c];
-    __syncthreads();
-    for (int at = threadIdx.x; at < R * CT * 32; at += kThreads) {
-        const int r = at / (32 * CT), c = at / 32 % CT, l = at & 31;     // lanes 0..31 hold gate rows, 32..63 up rows
-        const int t = 16 * c + (l & 15);
-        if (t >= ncols) continue;
-        const f32x4 gate = sum_waves(red, (r * CT + c) * 64 + l);
-        const f32x4 up = sum_waves(red, (r * CT + c) * 64 + l + 32);
-        f32x4 h;
+            for (int c = 0; c < CT; ++c) red[wave][(r * CT + c) * 64 + lane] = acc[r][c];
+        __syncthreads();
+        for (int at = threadIdx.x; at < R * CT * 32; at += kThreads) {
+            const int r = at / (32 * CT), c = at / 32 % CT, l = at & 31;     // lanes 0..31: gate rows, 32..63: up rows
+            const int t = col0 + XT * c + (l & 15) / (16 / XT);
+            if ((l & 15) % (16 / XT) || t >= ncols) continue;                // a repeated or an empty column
+            const f32x4 gate = sum_waves(red, (r * CT + c) * 64 + l);
+            const f32x4 up = sum_waves(red, (r * CT + c) * 64 + l + 32);
+            f32x4 h;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = gate[i] / (1.0f + __expf(-gate[i])) * up[i] * wt[t];
-        store4(a.h + (int64_t)slot[t] * a.I + i0 + 8 * r + 4 * (l >> 4), h);
+            for (int i = 0; i < 4; ++i) h[i] = gate[i] / (1.0f + __expf(-gate[i])) * up[i] * wt[t];
+            store4(a.h + (int64_t)slot[t] * a.I + i0 + 8 * r + 4 * (l >> 4), h);
+        }
     }
 }
 
 // Second launch: out[t] = sum over the experts of W2[e] h[t, e], one long product whose K runs over the experts
 // hit.  The sixteen columns are the tokens themselves (a token that does not name the expert reads zeros), so the
 // sum over experts stays in the accumulators and its order is fixed.
-template <int FMT, int G, int R, int CT>
+template <int FMT, int G, int R, int CT, int XT>
 __global__ void __launch_bounds__(kThreads)
 down_kernel(WView w, LayerArgs a) {
     __shared__ f32x4 red[kWaves][R * CT * 64];
+    __shared__ u32x4 corner[kWaves][kCorner];
     __shared__ uint32_t bits[kMaxLocal / 32];
     extern __shared__ int32_t ids[];         // [T * k]
     for (int i = threadIdx.x; i < a.T * a.k; i += kThreads) ids[i] = a.ids[i];
     expert_set(a, bits);
-    const int lane = lane_id(), wave = wave_index(), g = lane >> 4;
+    const int lane = lane_id(), wave = wave_index();
     const int row0 = blockIdx.x * (16 * R);
     const int64_t total = (int64_t)expert_count(bits) * w.nb;
-    const int64_t f0 = total * wave / kWaves;
-    const int n = (int)(total * (wave + 1) / kWaves - f0);
+    const int f0 = (int)(total * wave / kWaves);
+    const int n = (int)(total * (wave + 1) / kWaves) - f0;
 
     const __amdgpu_buffer_rsrc_t hb = row_buffer(a.h, (uint32_t)(a.T * a.k * a.I * 2));
     int e = 0, kb = 0;
     WView v = w;
-    TileRows<FMT, G> rows[R];
+    Tiles<FMT, G, R> tiles;
     uint32_t hrow[CT];
     uint32_t cols = 0;
     auto enter = [&](int expert) {           // this lane's rows and columns of an expert
         e = expert;
         v = expert_view<FMT, G>(w, e);
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            rows[r] = tile_rows<FMT, G>(v, row0 + 16 * r + (lane & 15), row0 + 16 * r + 4 * g);
+        tiles = tiles_of<FMT, G, R>(
+            v, [&](int t, int i) { return row0 + 16 * t + i; }, [&](int t, int i) { return row0 + 16 * t + 4 * i; });
         cols = 0;
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
-            const int t = 16 * c + (lane & 15);
+            const int t = XT * c + token_of_lane<XT>();
             hrow[c] = kNoRow;
             if (t < a.T)
                 for (int j = a.k - 1; j >= 0; --j)
@@ -285,23 +290,22 @@ down_kernel(WView w, LayerArgs a) {
         }
     };
     if (n > 0) {
-        kb = (int)(f0 % w.nb);
-        enter(nth_expert(bits, (int)(f0 / w.nb)));
+        kb = f0 % w.nb;
+        enter(nth_expert(bits, f0 / w.nb));
     }
     f32x4 acc[R][CT] = {};
-    stream_blocks<FMT, G, R, CT>(n, [&](Step<FMT, G, R, CT>& st) {
+    stream_blocks<FMT, G, R, CT, XT>(n, [&](Step<FMT, G, R, CT, XT>& st) {
         if (kb == w.nb) {
             kb = 0;
             enter(next_expert(bits, e));
         }
-#pragma unroll
-        for (int r = 0; r < R; ++r) load_weights<FMT, G>(rows[r], v, kb, st.w[r], st.s[r]);
+        load_weights<FMT, G, R>(tiles, v, kb, st.w, st.s);
 #pragma unroll
         for (int c = 0; c < CT; ++c)
-            if (CT == 1 || (cols >> c & 1)) load_rows<FMT, G>(hb, hrow[c], kb, st.x[c]);
+            if (CT == 1 || (cols >> c & 1)) load_rows<FMT, G, XT>(hb, hrow[c], kb, st.x[c]);
         ++kb;
         return cols;
-    }, acc);
+    }, corner[wave], acc);
 
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -310,7 +314,8 @@ down_kernel(WView w, LayerArgs a) {
     __syncthreads();
     for (int at = threadIdx.x; at < R * CT * 64; at += kThreads) {
         const int r = at / (64 * CT), c = at / 64 % CT, l = at & 63;
-        const int t = 16 * c + (l & 15);
+        const int t = XT * c + (l & 15) / (16 / XT);
+        if ((l & 15) % (16 / XT)) continue;              // a repeated column
         if (t < a.T) store4(a.out + (int64_t)t * a.H + row0 + 16 * r + 4 * (l >> 4), sum_waves(red, at));
     }
 }
@@ -358,12 +363,30 @@ moe_status with_format(int format, int groups, F&& f) {
     return f(std::integral_constant<int, MOE_W_INT4>{}, std::integral_constant<int, 4>{});
 }
 
-// Column tiles a launch covers: 1, 2 or 4.
+// Calls f(column tiles, tokens of a tile) for the tokens of a launch.
 template <class F>
 void with_cols(int64_t tokens, F&& f) {
-    if (tokens <= 16) f(std::integral_constant<int, 1>{});
-    else if (tokens <= 32) f(std::integral_constant<int, 2>{});
-    else f(std::integral_constant<int, 4>{});
+    if (tokens <= 4) f(std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
+    else if (tokens <= 8) f(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{});
+    else if (tokens <= 16) f(std::integral_constant<int, 1>{}, std::integral_constant<int, 16>{});
+    else if (tokens <= 32) f(std::integral_constant<int, 2>{}, std::integral_constant<int, 16>{});
+    else f(std::integral_constant<int, 4>{}, std::integral_constant<int, 16>{});
+}
+
+template <int... Rs, class F>
+void with_rows(int r, F&& f) {
+    ((r == Rs ? f(std::integral_constant<int, Rs>{}) : void()), ...);
+}
+
+constexpr int kCus = 256;
+
+// Row tiles of a wavefront: the more, the fewer token loads a weight load takes beside it, as long as there is a
+// workgroup for every CU.
+int matvec_rows(int64_t n, int64_t m) {
+    const int most = m > 32 ? 1 : m > 16 ? 2 : 4;
+    int r = 1;
+    while (r < most && n >= 16 * 2 * r * kCus) r *= 2;
+    return r;
 }
 
 }  // namespace
@@ -382,10 +405,15 @@ extern "C" moe_status moe_matvec(int32_t m, int32_t n, int32_t k, const uint16_t
     if (x_stride >= (1 << 24)) return MOE_ERR_UNSUPPORTED;
     hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
     return with_format(w->format, groups, [&](auto fmt, auto g) {
-        with_cols(m, [&](auto ct) {
-            constexpr int R = 1;
-            const dim3 grid((unsigned)((n + 16 * R - 1) / (16 * R)), (unsigned)((m + 16 * ct - 1) / (16 * ct)));
-            matvec_kernel<fmt, g, R, ct><<<grid, kThreads, 0, stream>>>(v, x_bf16, x_stride, m, y_bf16, y_stride);
+        with_cols(m, [&](auto ct, auto xt) {
+            const auto launch = [&](auto r) {
+                const dim3 grid((unsigned)((n + 16 * r - 1) / (16 * r)), (unsigned)((m + xt * ct - 1) / (xt * ct)));
+                matvec_kernel<fmt, g, r, ct, xt><<<grid, kThreads, 0, stream>>>(v, x_bf16, x_stride, m, y_bf16,
+                                                                               y_stride);
+            };
+            if constexpr (ct == 1) with_rows<1, 2, 4>(matvec_rows(n, m), launch);
+            else if constexpr (ct == 2) with_rows<1, 2>(matvec_rows(n, m), launch);
+            else launch(std::integral_constant<int, 1>{});
         });
         return launch_status();
     });
@@ -434,19 +462,30 @@ extern "C" moe_status moe_few_token_layer(const moe_dims* dims, int32_t inter, c
         a.out = out_bf16 + t0 * d.H;
         a.T = (int)std::min<int64_t>(d.T - t0, kChunk);
         a.k = (int)d.k, a.e0 = (int)d.e0, a.L = (int)d.L, a.H = (int)d.H, a.I = inter;
+        // columns for twice the tokens that an expert can expect; an expert with more takes another pass
+        const int64_t share = a.T <= 16 ? a.T : std::min<int64_t>(std::max<int64_t>(2 * a.T * d.k / d.E, 9), 32);
+        // workgroups of one row tile that uniform routing would keep busy
+        const double hit = d.L * (1.0 - std::pow(1.0 - (double)d.k / d.E, (double)a.T));
+        const int64_t busy = (int64_t)(hit * (inter / 8));
+        const int r1 = busy >= 4 * kCus ? 4 : busy >= 2 * kCus ? 2 : 1;
         st = with_format(w1->format, g1, [&](auto fmt, auto g) {
-            with_cols(a.T, [&](auto ct) {
-                constexpr int R = 1;
-                const dim3 grid((unsigned)(inter / (8 * R)), (unsigned)std::min<int64_t>(a.T * d.k, d.L));
-                gate_up_kernel<fmt, g, R, ct><<<grid, kThreads, 0, stream>>>(v1, a);
+            with_cols(share, [&](auto ct, auto xt) {
+                if constexpr (ct <= 2)
+                    with_rows<1, 2, 4>(r1, [&](auto r) {
+                        const dim3 grid((unsigned)(inter / (8 * r)), (unsigned)std::min<int64_t>(a.T * d.k, d.L));
+                        gate_up_kernel<fmt, g, r, ct, xt><<<grid, kThreads, 0, stream>>>(v1, a);
+                    });
             });
             return launch_status();
         });
         if (st != MOE_OK) return st;
+        const int r2 = d.H >= 24 * kCus ? 2 : 1;
         st = with_format(w2->format, g2, [&](auto fmt, auto g) {
-            with_cols(a.T, [&](auto ct) {
-                constexpr int R = 1;
-                down_kernel<fmt, g, R, ct><<<dim3((unsigned)(d.H / (16 * R))), kThreads, a.T * a.k * 4, stream>>>(v2, a);
+            with_cols(a.T, [&](auto ct, auto xt) {
+                with_rows<1, 2>(r2, [&](auto r) {
+                    down_kernel<fmt, g, r, ct, xt><<<dim3((unsigned)(d.H / (16 * r))), kThreads, a.T * a.k * 4, stream>>>(
+                        v2, a);
+                });
             });
             return launch_status();
         });

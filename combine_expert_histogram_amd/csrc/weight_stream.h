@@ -47,8 +47,13 @@ struct Fmt {
     static constexpr int kLoads = kFour ? 1 : 2;             // 16 B loads a lane, block and tile
 };
 
+// The scales of R tiles and one block, one load for all of them: the sixteen lanes that would repeat one tile's
+// scales fetch other tiles' instead, and tile_scales hands them round.
+//   e4m3: the R tiles lie in one 128-row scale block, so every lane's own word serves all of them.
+//   MX:   lane l fetches the word of row l % 16 of tile (l / 16) % R.
+//   int4: lane l fetches the four rows 4 (l / 16) .. + 3 of tile (l % 16) % R.
 template <int FMT, int G>
-struct Scales {                                              // of one tile and block, as loaded
+struct Scales {
     uint32_t w;                                              // MX codes, or the fp32 scale's bits
 };
 template <int G>
@@ -57,47 +62,72 @@ struct Scales<MOE_W_INT4, G> {
     uint32_t z[G];                                           // 4 rows x G bytes
 };
 
-// The sixteen rows of a tile, as one lane addresses them.
-template <int FMT, int G>
-struct TileRows {
-    const uint8_t* w;        // the lane's A row, at its 16 B
+// A memory instruction costs its CU one cycle for every run of adjacent lanes that reads within 64 B.  In the MFMA
+// layout adjacent lanes hold different rows, which makes 64 such runs of 16 B; so the four lanes 4 r .. 4 r + 3 fetch
+// 64 B of row r, and the wavefront turns the 1 KiB piece into the MFMA layout through its own corner of LDS (LDS
+// instructions of one wavefront stay in order, so this takes no barrier).  The swizzle makes both the writes (eight
+// lanes: two rows) and the reads (eight lanes: one 16 B column of eight rows) fall on distinct banks.
+constexpr int kCorner = 4 * 64;                              // 16 B elements of a wavefront's corner
+
+__device__ __forceinline__ int turn_slot(int row, int piece) { return row * 4 + (piece ^ (row >> 1 & 3)); }
+
+__device__ __forceinline__ void turn_in(u32x4* lds, const u32x4& v) {
+    const int l = lane_id();
+    lds[turn_slot(l >> 2, l & 3)] = v;
+}
+__device__ __forceinline__ u32x4 turn_out(const u32x4* lds, int piece) { return lds[turn_slot(lane_id() & 15, piece)]; }
+
+// R tiles of sixteen rows, as one lane addresses them.
+template <int FMT, int G, int R>
+struct Tiles {
+    const uint8_t* w[R];     // row lane / 4 of each tile, at 16 B piece lane % 4
     const uint8_t* s;        // block 0's scales
     const uint8_t* z;
 };
 
-// arow: the lane's weight row (its A row); drow: the first of the four rows the lane's results belong to.
-template <int FMT, int G>
-__device__ __forceinline__ TileRows<FMT, G> tile_rows(const WView& v, int64_t arow, int64_t drow) {
+// a_row(t, i): the weight row in row i of tile t;  d_row(t, i): the first of the four rows of tile t that a lane of
+// group i = lane / 16 holds results of.
+template <int FMT, int G, int R, class ARow, class DRow>
+__device__ __forceinline__ Tiles<FMT, G, R> tiles_of(const WView& v, ARow&& a_row, DRow&& d_row) {
     using F = Fmt<FMT, G>;
-    const int g = lane_id() >> 4;
-    TileRows<FMT, G> t;
-    t.w = v.data + arow * (int64_t)v.nb * F::kRowBytes + 16 * g;
+    const int l = lane_id(), g = l >> 4, c = l & 15;
+    Tiles<FMT, G, R> t;
+#pragma unroll
+    for (int r = 0; r < R; ++r) t.w[r] = v.data + (int64_t)a_row(r, l >> 2) * v.nb * F::kRowBytes + 16 * (l & 3);
     t.z = nullptr;
+    const uint8_t* s = static_cast<const uint8_t*>(v.scale);
     if constexpr (F::kInt4) {
-        t.s = static_cast<const uint8_t*>(v.scale) + drow * 2 * G;
-        if (v.zero) t.z = v.zero + drow * G;
+        const int64_t row = d_row(c % R, g);
+        t.s = s + row * 2 * G;
+        if (v.zero) t.z = v.zero + row * G;
     } else if constexpr (F::kMx) {
-        t.s = static_cast<const uint8_t*>(v.scale) + arow * 4;
+        t.s = s + (int64_t)a_row(g % R, c) * 4;
     } else {
-        t.s = static_cast<const uint8_t*>(v.scale) + (drow / 128) * (int64_t)v.nb * 4;
+        t.s = s + (int64_t)(d_row(0, g) / 128) * v.nb * 4;
     }
     return t;
 }
 
-template <int FMT, int G, int R, int CT>
+// A column tile of XT = 4, 8 or 16 tokens: with fewer than sixteen, token t owns the 16 / XT columns from t * 16 / XT,
+// its lanes fetch different parts of the token's values and a quad permutation hands them round, so a block takes
+// XT / 4 loads instead of four.
+template <int FMT, int G, int R, int CT, int XT>
 struct Step {                                                // one K block in flight
     u32x4 w[R][Fmt<FMT, G>::kLoads];
-    Scales<FMT, G> s[R];
-    u32x4 x[CT][4];
+    Scales<FMT, G> s;
+    u32x4 x[CT][XT / 4];
 };
 
-template <int FMT, int G>
-__device__ __forceinline__ void load_weights(const TileRows<FMT, G>& t, const WView& v, int kb,
-                                             u32x4 (&w)[Fmt<FMT, G>::kLoads], Scales<FMT, G>& s) {
+template <int FMT, int G, int R>
+__device__ __forceinline__ void load_weights(const Tiles<FMT, G, R>& t, const WView& v, int kb,
+                                             u32x4 (&w)[R][Fmt<FMT, G>::kLoads], Scales<FMT, G>& s) {
     using F = Fmt<FMT, G>;
-    const u32x4* p = reinterpret_cast<const u32x4*>(t.w + (int64_t)kb * F::kRowBytes);
 #pragma unroll
-    for (int i = 0; i < F::kLoads; ++i) w[i] = __builtin_nontemporal_load(p + 4 * i);
+    for (int r = 0; r < R; ++r) {
+        const u32x4* p = reinterpret_cast<const u32x4*>(t.w[r] + (int64_t)kb * F::kRowBytes);
+#pragma unroll
+        for (int i = 0; i < F::kLoads; ++i) w[r][i] = p[4 * i];
+    }
     if constexpr (F::kInt4) {
         const int64_t at = (int64_t)kb * v.n;
         const uint8_t* ps = t.s + at * 2 * G;
@@ -111,7 +141,7 @@ __device__ __forceinline__ void load_weights(const TileRows<FMT, G>& t, const WV
                 s.s[4 * i] = a.x, s.s[4 * i + 1] = a.y, s.s[4 * i + 2] = a.z, s.s[4 * i + 3] = a.w;
             }
         }
-        if (t.z) {
+        if (v.zero) {
             const uint8_t* pz = t.z + at * G;
             if constexpr (G == 1) {
                 s.z[0] = *reinterpret_cast<const uint32_t*>(pz);
@@ -133,6 +163,42 @@ __device__ __forceinline__ void load_weights(const TileRows<FMT, G>& t, const WV
     }
 }
 
+// MX: tile t's word of this lane's row, from the lanes that fetched it.
+template <int R>
+__device__ __forceinline__ void spread_rows(uint32_t w, uint32_t (&o)[R]) {
+    static_assert(R == 1 || R == 2 || R == 4, "tiles");
+    if constexpr (R == 1) {
+        o[0] = w;
+    } else if constexpr (R == 2) {                           // rows of lanes [0 1 0 1] -> [0 0 0 0], [1 1 1 1]
+        const auto p = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+        o[0] = p[0], o[1] = p[1];
+    } else {                                                 // [0 1 2 3] -> [0 1 0 1], [2 3 2 3], then as above
+        const auto h = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+        const auto p = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+        const auto q = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+        o[0] = p[0], o[1] = p[1], o[2] = q[0], o[3] = q[1];
+    }
+}
+
+// int4: the word that lane t of each sixteen holds
+template <int T>
+__device__ __forceinline__ uint32_t row_lane(uint32_t w) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)w, 0x150 + T, 0xF, 0xF, false);    // row_newbcast
+}
+
+template <int G, int R, int T = 0>
+__device__ __forceinline__ void spread_lanes(const Scales<MOE_W_INT4, G>& s, Scales<MOE_W_INT4, G> (&o)[R]) {
+    if constexpr (R == 1) {
+        o[0] = s;
+    } else if constexpr (T < R) {
+#pragma unroll
+        for (int i = 0; i < 2 * G; ++i) o[T].s[i] = row_lane<T>(s.s[i]);
+#pragma unroll
+        for (int i = 0; i < G; ++i) o[T].z[i] = row_lane<T>(s.z[i]);
+        spread_lanes<G, R, T + 1>(s, o);
+    }
+}
+
 // Element offset, inside a block, of the eight x values that MFMA q of the lane group g multiplies.
 template <int FMT, int G>
 __device__ __forceinline__ int x_offset(int q, int g) {
@@ -140,6 +206,29 @@ __device__ __forceinline__ int x_offset(int q, int g) {
     if constexpr (F::kInt4) return 32 * q + 8 * g;
     if constexpr (F::kFour) return 32 * g + 8 * q;
     return 64 * (q >> 1) + 16 * g + 8 * (q & 1);
+}
+
+template <int CTRL>
+__device__ __forceinline__ u32x4 quad_perm(const u32x4& v) {
+    u32x4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = (uint32_t)__builtin_amdgcn_mov_dpp((int)v[i], CTRL, 0xF, 0xF, true);
+    return o;
+}
+
+// The eight token values of MFMA q of a block (q a constant after unrolling).
+template <int XT>
+__device__ __forceinline__ bf16x8 token_values(const u32x4 (&x)[XT / 4], int q) {
+    u32x4 v;
+    if constexpr (XT == 16) {
+        v = x[q];
+    } else if constexpr (XT == 8) {
+        v = q & 1 ? quad_perm<0xF5>(x[q >> 1]) : quad_perm<0xA0>(x[q >> 1]);    // lanes 1 1 3 3 or 0 0 2 2
+    } else {
+        v = q == 0 ? quad_perm<0x00>(x[0]) : q == 1 ? quad_perm<0x55>(x[0])
+                                         : q == 2 ? quad_perm<0xAA>(x[0]) : quad_perm<0xFF>(x[0]);
+    }
+    return __builtin_bit_cast(bf16x8, v);
 }
 
 // The eight bf16 values of MFMA q of a block (exact).  int4 gives 128 + code.
@@ -183,17 +272,42 @@ __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
 // short of the last two MFMAs).  The asm ties the wait to the values, so no branch can come between.
 template <int N>
 __device__ __forceinline__ void settle(f32x4 (&d)[N]) {
-    static_assert(N >= 1 && N <= 4, "tiles");
+    static_assert(N >= 1 && N <= 5, "tiles");
     if constexpr (N == 1) asm volatile("s_nop 15" : "+v"(d[0]));
     if constexpr (N == 2) asm volatile("s_nop 15" : "+v"(d[0]), "+v"(d[1]));
     if constexpr (N == 3) asm volatile("s_nop 15" : "+v"(d[0]), "+v"(d[1]), "+v"(d[2]));
     if constexpr (N == 4) asm volatile("s_nop 15" : "+v"(d[0]), "+v"(d[1]), "+v"(d[2]), "+v"(d[3]));
+    if constexpr (N == 5)
+        asm volatile("s_nop 15" : "+v"(d[0]), "+v"(d[1]), "+v"(d[2]), "+v"(d[3]), "+v"(d[4]));
 }
 
 // acc += one K block.  cols: bit c set where column tile c has a token (uniform over the wavefront).
-template <int FMT, int G, int R, int CT>
-__device__ __forceinline__ void block_product(const Step<FMT, G, R, CT>& st, uint32_t cols, f32x4 (&acc)[R][CT]) {
+template <int FMT, int G, int R, int CT, int XT>
+__device__ __forceinline__ void block_product(Step<FMT, G, R, CT, XT>& st, uint32_t cols, u32x4* corner,
+                                              f32x4 (&acc)[R][CT]) {
     using F = Fmt<FMT, G>;
+    constexpr int kBuf = kCorner / 64;                       // 1 KiB pieces that fit the corner
+    if constexpr (XT == 16) {
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+            if (CT > 1 && !(cols >> c & 1)) continue;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) turn_in(corner + 64 * q, st.x[c][q]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int piece = x_offset<FMT, G>(q, lane_id() >> 4) / 8;       // of the block's sixteen 16 B pieces
+                st.x[c][q] = turn_out(corner + (piece >> 2) * 64, piece & 3);
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; r += kBuf / F::kLoads) {
+#pragma unroll
+        for (int p = 0; p < kBuf && p < R * F::kLoads; ++p) turn_in(corner + 64 * p, st.w[r + p / F::kLoads][p % F::kLoads]);
+#pragma unroll
+        for (int p = 0; p < kBuf && p < R * F::kLoads; ++p)
+            st.w[r + p / F::kLoads][p % F::kLoads] = turn_out(corner + 64 * p, lane_id() >> 4);
+    }
     const int g = lane_id() >> 4;
     const f32x4 none = {0.f, 0.f, 0.f, 0.f};
     if constexpr (F::kInt4) {
@@ -201,6 +315,8 @@ __device__ __forceinline__ void block_product(const Step<FMT, G, R, CT>& st, uin
         const u32x4 ones_bits = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
         const bf16x8 ones = __builtin_bit_cast(bf16x8, ones_bits);
         constexpr int Q = 4 / G;                             // MFMAs per group
+        Scales<FMT, G> sc[R];
+        spread_lanes<G, R>(st.s, sc);
 #pragma unroll
         for (int h = 0; h < G; ++h) {
             bf16x8 a[R][Q];
@@ -216,7 +332,7 @@ __device__ __forceinline__ void block_product(const Step<FMT, G, R, CT>& st, uin
                 for (int r = 0; r <= R; ++r) d[r] = none;
 #pragma unroll
                 for (int q = 0; q < Q; ++q) {
-                    const bf16x8 b = __builtin_bit_cast(bf16x8, st.x[c][h * Q + q]);
+                    const bf16x8 b = token_values<XT>(st.x[c], h * Q + q);
                     d[R] = mfma(ones, b, d[R]);
 #pragma unroll
                     for (int r = 0; r < R; ++r) d[r] = mfma(a[r][q], b, d[r]);
@@ -227,21 +343,24 @@ __device__ __forceinline__ void block_product(const Step<FMT, G, R, CT>& st, uin
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int at = i * G + h;            // row i of the four, group h of the block
-                        const uint32_t sw = st.s[r].s[at >> 1];
+                        const uint32_t sw = sc[r].s[at >> 1];
                         const float s = at & 1 ? bf16_hi(sw) : bf16_lo(sw);
-                        const float z = 128.0f + (float)((st.s[r].z[at >> 2] >> (8 * (at & 3))) & 0xFFu);
+                        const uint32_t zw = sc[r].z[at >> 2] | 0x80808080u;      // 128 + zero
+                        const float z = (float)((zw >> (8 * (at & 3))) & 0xFFu);
                         acc[r][c][i] = fmaf(s, fmaf(-z, d[R][i], d[r][i]), acc[r][c][i]);
                     }
             }
         }
     } else {
         bf16x8 a[R][4];
+        uint32_t words[R];
+        if constexpr (F::kMx) spread_rows<R>(st.s.w, words);
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 float mx = 1.0f;
-                if constexpr (F::kMx) mx = e8m0_value(st.s[r].w, F::kFour ? g : 2 * (q >> 1) + (g >> 1));
+                if constexpr (F::kMx) mx = e8m0_value(words[r], F::kFour ? g : 2 * (q >> 1) + (g >> 1));
                 a[r][q] = widen<FMT, G>(st.w[r], mx, q);
             }
 #pragma unroll
@@ -251,16 +370,18 @@ __device__ __forceinline__ void block_product(const Step<FMT, G, R, CT>& st, uin
 #pragma unroll
             for (int r = 0; r < R; ++r) d[r] = F::kMx ? acc[r][c] : none;
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 4; ++q) {
+                const bf16x8 b = token_values<XT>(st.x[c], q);
 #pragma unroll
-                for (int r = 0; r < R; ++r) d[r] = mfma(a[r][q], __builtin_bit_cast(bf16x8, st.x[c][q]), d[r]);
+                for (int r = 0; r < R; ++r) d[r] = mfma(a[r][q], b, d[r]);
+            }
             settle(d);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 if constexpr (F::kMx) {
                     acc[r][c] = d[r];
                 } else {
-                    const float s = __uint_as_float(st.s[r].w);
+                    const float s = __uint_as_float(st.s.w);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[r][c][i] = fmaf(s, d[r][i], acc[r][c][i]);
                 }
@@ -277,13 +398,24 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const void* base, u
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
 }
 
-template <int FMT, int G>
-__device__ __forceinline__ void load_rows(__amdgpu_buffer_rsrc_t rows, uint32_t row_bytes, int kb, u32x4 (&x)[4]) {
-    const int g = lane_id() >> 4;
+// row_bytes: where the row of the lane's token starts, or kNoRow.  A tile of sixteen is fetched like weights (token
+// lane / 4) and turned in block_product.
+template <int XT>
+__device__ __forceinline__ int token_of_lane() {
+    const int l = lane_id();
+    return XT == 16 ? l >> 2 : (l & 15) / (16 / XT);
+}
+
+template <int FMT, int G, int XT>
+__device__ __forceinline__ void load_rows(__amdgpu_buffer_rsrc_t rows, uint32_t row_bytes, int kb,
+                                          u32x4 (&x)[XT / 4]) {
+    constexpr int S = 16 / XT;
+    const int l = lane_id(), g = l >> 4, sub = l % S;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-        x[q] = __builtin_amdgcn_raw_buffer_load_b128(
-            rows, row_bytes + 2u * (uint32_t)(x_offset<FMT, G>(q, g)), kb * (2 * kKBlock), 0);
+    for (int i = 0; i < XT / 4; ++i) {
+        const uint32_t at = XT == 16 ? 64 * i + 16 * (l & 3) : 2 * x_offset<FMT, G>(i * S + sub, g);
+        x[i] = __builtin_amdgcn_raw_buffer_load_b128(rows, row_bytes + at, kb * (2 * kKBlock), 0);
+    }
 }
 
 }  // namespace moe
