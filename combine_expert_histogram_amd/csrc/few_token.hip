@@ -13,7 +13,7 @@ using namespace moe;
 constexpr int kWaves = 8;                  // wavefronts of a workgroup; they split the K blocks
 constexpr int kThreads = kWaves * MOE_WAVE;
 // K blocks a wavefront keeps in flight
-constexpr int depth_of(int R, int CT) { return CT > 2 || R == 4 ? 1 : CT == 2 || R == 2 ? 2 : 4; }
+constexpr int depth_of(int R, int CT) { return CT > 1 || R == 4 ? 1 : R == 2 ? 2 : 4; }
 constexpr int kChunk = 64;                 // tokens a layer launch handles: one lane each, four column tiles
 constexpr int kMaxTopK = 64;
 constexpr int kMaxLocal = 1024;
@@ -102,6 +102,90 @@ matvec_kernel(WView w, const uint16_t* __restrict__ x, int64_t ldx, int M, uint1
         const int t = XT * c + (l & 15) / (16 / XT);
         if ((l & 15) % (16 / XT)) continue;              // a repeated column
         if (t < ncols && row < w.n) store4(y + (col0 + t) * ldy + row, sum_waves(red, at));
+    }
+}
+
+// More than sixteen tokens against many rows: here the tokens' values are the larger stream (sixteen rows of 64 tokens
+// read 16 KiB of them beside 1 or 2 KiB of weights), so the eight wavefronts share them.  Each takes 16 R rows over the
+// whole of K; a block's token values go through LDS once (two buffers, one barrier a block), and the weights of two
+// blocks are in flight in registers.
+template <int FMT, int G, int R, int CT>
+__global__ void __launch_bounds__(kThreads)
+matvec_wide_kernel(WView w, const uint16_t* __restrict__ x, int64_t ldx, int M, uint16_t* __restrict__ y, int64_t ldy) {
+    using F = Fmt<FMT, G>;
+    constexpr int kPieces = CT * 16 * 16;                    // 16 B pieces of a block's token values
+    constexpr int kMine = kPieces / kThreads;
+    __shared__ u32x4 xs[2][kPieces];
+    __shared__ u32x4 corner[kWaves][kCorner];
+    const int lane = lane_id(), wave = wave_index();
+    const int64_t row0 = ((int64_t)blockIdx.x * kWaves + wave) * (16 * R);
+    const int64_t col0 = (int64_t)blockIdx.y * (16 * CT);
+    const int ncols = (int)min<int64_t>(M - col0, 16 * CT);
+
+    // rows past n repeat the last ones and are not stored
+    const Tiles<FMT, G, R> tiles = tiles_of<FMT, G, R>(
+        w, [&](int t, int i) { return min(row0 + 16 * t + i, w.n - 1); },
+        [&](int t, int i) { return min(row0 + 16 * t + 4 * i, w.n - 4); });
+    const __amdgpu_buffer_rsrc_t xb =
+        row_buffer(x + col0 * ldx, (uint32_t)(((int64_t)(ncols - 1) * ldx + (int64_t)w.nb * kKBlock) * 2));
+    uint32_t at[kMine];                                      // piece p of token t: t * 16 + (p ^ t % 8)
+    int to[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int id = threadIdx.x + kThreads * i, t = id >> 4, p = id & 15;
+        at[i] = t < ncols ? (uint32_t)(t * ldx * 2 + 16 * p) : kNoRow;
+        to[i] = t * 16 + (p ^ (t & 7));
+    }
+    u32x4 xr[kMine];
+    const auto load_x = [&](int kb) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+            xr[i] = __builtin_amdgcn_raw_buffer_load_b128(xb, at[i], kb * (2 * kKBlock), 0);
+    };
+    const auto put_x = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) xs[buf][to[i]] = xr[i];
+    };
+
+    u32x4 wr[2][R][F::kLoads];
+    Scales<FMT, G> sc[2];
+    load_x(0);
+    load_weights<FMT, G, R>(tiles, w, 0, wr[0], sc[0]);
+    put_x(0);
+    if (w.nb > 1) {
+        load_weights<FMT, G, R>(tiles, w, 1, wr[1], sc[1]);
+        load_x(1);
+    }
+    lds_barrier();
+    f32x4 acc[R][CT] = {};
+    for (int kb0 = 0; kb0 < w.nb; kb0 += 2) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int kb = kb0 + u;
+            if (kb >= w.nb) break;
+            turn_weights<FMT, G, R>(corner[wave], wr[u]);
+            u32x4 wt[R][F::kLoads];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int p = 0; p < F::kLoads; ++p) wt[r][p] = wr[u][r][p];
+            const Scales<FMT, G> s = sc[u];
+            if (kb + 2 < w.nb) load_weights<FMT, G, R>(tiles, w, kb + 2, wr[u], sc[u]);
+            if (kb + 1 < w.nb) put_x(1 - u);
+            if (kb + 2 < w.nb) load_x(kb + 2);
+            shared_product<FMT, G, R, CT>(wt, s, xs[u], acc);
+            // block kb's tokens are read and block kb + 1's are written, on both sides of it
+            lds_barrier();
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+        const int t = 16 * c + (lane & 15);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t row = row0 + 16 * r + 4 * (lane >> 4);
+            if (t < ncols && row < w.n) store4(y + (col0 + t) * ldy + row, acc[r][c]);
+        }
     }
 }
 
@@ -380,12 +464,17 @@ void with_rows(int r, F&& f) {
 
 constexpr int kCus = 256;
 
+// Row tiles of a wavefront of the wide product, and whether it pays: its workgroups take 256 rows each and need most
+// of the CUs, while the plain form's token traffic grows with the column tiles (the figures are beside moe_matvec).
+constexpr int kWideRows = 2;
+constexpr int64_t kWideGroupRows = kWaves * 16 * kWideRows;
+bool wide_pays(int64_t n, int64_t m) { return m > 16 && n >= kCus * kWideGroupRows; }
+
 // Row tiles of a wavefront: the more, the fewer token loads a weight load takes beside it, as long as there is a
 // workgroup for every CU.
-int matvec_rows(int64_t n, int64_t m) {
-    const int most = m > 32 ? 1 : m > 16 ? 2 : 4;
+int matvec_rows(int64_t n) {
     int r = 1;
-    while (r < most && n >= 16 * 2 * r * kCus) r *= 2;
+    while (r < 4 && n >= 16 * 2 * r * kCus) r *= 2;
     return r;
 }
 
@@ -405,15 +494,24 @@ extern "C" moe_status moe_matvec(int32_t m, int32_t n, int32_t k, const uint16_t
     if (x_stride >= (1 << 24)) return MOE_ERR_UNSUPPORTED;
     hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
     return with_format(w->format, groups, [&](auto fmt, auto g) {
+        if (wide_pays(n, m)) {
+            const auto launch = [&](auto ct) {
+                const dim3 grid((unsigned)((n + kWideGroupRows - 1) / kWideGroupRows),
+                                (unsigned)((m + 16 * ct - 1) / (16 * ct)));
+                matvec_wide_kernel<fmt, g, kWideRows, ct><<<grid, kThreads, 0, stream>>>(v, x_bf16, x_stride, m, y_bf16,
+                                                                                        y_stride);
+            };
+            if (m <= 32) launch(std::integral_constant<int, 2>{});
+            else launch(std::integral_constant<int, 4>{});
+            return launch_status();
+        }
         with_cols(m, [&](auto ct, auto xt) {
             const auto launch = [&](auto r) {
                 const dim3 grid((unsigned)((n + 16 * r - 1) / (16 * r)), (unsigned)((m + xt * ct - 1) / (xt * ct)));
                 matvec_kernel<fmt, g, r, ct, xt><<<grid, kThreads, 0, stream>>>(v, x_bf16, x_stride, m, y_bf16,
                                                                                y_stride);
             };
-            if constexpr (ct == 1) with_rows<1, 2, 4>(matvec_rows(n, m), launch);
-            else if constexpr (ct == 2) with_rows<1, 2>(matvec_rows(n, m), launch);
-            else launch(std::integral_constant<int, 1>{});
+            with_rows<1, 2, 4>(matvec_rows(n), launch);
         });
         return launch_status();
     });

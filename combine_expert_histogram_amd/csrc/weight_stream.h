@@ -281,12 +281,24 @@ __device__ __forceinline__ void settle(f32x4 (&d)[N]) {
         asm volatile("s_nop 15" : "+v"(d[0]), "+v"(d[1]), "+v"(d[2]), "+v"(d[3]), "+v"(d[4]));
 }
 
+// Fetched pieces of R tiles into the MFMA layout.
+template <int FMT, int G, int R>
+__device__ __forceinline__ void turn_weights(u32x4* corner, u32x4 (&w)[R][Fmt<FMT, G>::kLoads]) {
+    constexpr int L = Fmt<FMT, G>::kLoads, kBuf = R * L < kCorner / 64 ? R * L : kCorner / 64;
+#pragma unroll
+    for (int r = 0; r < R; r += kBuf / L) {
+#pragma unroll
+        for (int p = 0; p < kBuf; ++p) turn_in(corner + 64 * p, w[r + p / L][p % L]);
+#pragma unroll
+        for (int p = 0; p < kBuf; ++p) w[r + p / L][p % L] = turn_out(corner + 64 * p, lane_id() >> 4);
+    }
+}
+
 // acc += one K block.  cols: bit c set where column tile c has a token (uniform over the wavefront).
 template <int FMT, int G, int R, int CT, int XT>
 __device__ __forceinline__ void block_product(Step<FMT, G, R, CT, XT>& st, uint32_t cols, u32x4* corner,
                                               f32x4 (&acc)[R][CT]) {
     using F = Fmt<FMT, G>;
-    constexpr int kBuf = kCorner / 64;                       // 1 KiB pieces that fit the corner
     if constexpr (XT == 16) {
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
@@ -300,14 +312,7 @@ __device__ __forceinline__ void block_product(Step<FMT, G, R, CT, XT>& st, uint3
             }
         }
     }
-#pragma unroll
-    for (int r = 0; r < R; r += kBuf / F::kLoads) {
-#pragma unroll
-        for (int p = 0; p < kBuf && p < R * F::kLoads; ++p) turn_in(corner + 64 * p, st.w[r + p / F::kLoads][p % F::kLoads]);
-#pragma unroll
-        for (int p = 0; p < kBuf && p < R * F::kLoads; ++p)
-            st.w[r + p / F::kLoads][p % F::kLoads] = turn_out(corner + 64 * p, lane_id() >> 4);
-    }
+    turn_weights<FMT, G, R>(corner, st.w);
     const int g = lane_id() >> 4;
     const f32x4 none = {0.f, 0.f, 0.f, 0.f};
     if constexpr (F::kInt4) {
@@ -388,6 +393,112 @@ __device__ __forceinline__ void block_product(Step<FMT, G, R, CT, XT>& st, uint3
             }
         }
     }
+}
+
+// Ties the values of several tiles down before one wait for all of them.
+template <int R, int N>
+__device__ __forceinline__ void settle_all(f32x4 (&d)[R][N]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < N; ++c) asm volatile("" : "+v"(d[r][c]));
+    asm volatile("s_nop 15" : "+v"(d[0][0]));
+}
+
+// acc += one K block of weights in the MFMA layout times the tokens that the workgroup shares in LDS (piece p of token
+// t in element 16 t + (p ^ t % 8): eight lanes that read one piece of eight tokens meet eight distinct banks).
+template <int FMT, int G, int R, int CT>
+__device__ __forceinline__ void shared_product(const u32x4 (&w)[R][Fmt<FMT, G>::kLoads], const Scales<FMT, G>& s,
+                                               const u32x4* xs, f32x4 (&acc)[R][CT]) {
+    using F = Fmt<FMT, G>;
+    const int l = lane_id(), c16 = l & 15, g = l >> 4;
+    const f32x4 none = {0.f, 0.f, 0.f, 0.f};
+    const auto tokens = [&](int c, int q) {
+        const int piece = x_offset<FMT, G>(q, g) / 8;
+        return __builtin_bit_cast(bf16x8, xs[(16 * c + c16) * 16 + (piece ^ (c16 & 7))]);
+    };
+    if constexpr (F::kInt4) {
+        const u32x4 ones_bits = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+        const bf16x8 ones = __builtin_bit_cast(bf16x8, ones_bits);
+        constexpr int Q = 4 / G;
+        Scales<FMT, G> sc[R];
+        spread_lanes<G, R>(s, sc);
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+            f32x4 d[R + 1][CT];                              // the last row: sum x
+#pragma unroll
+            for (int r = 0; r <= R; ++r)
+#pragma unroll
+                for (int c = 0; c < CT; ++c) d[r][c] = none;
+#pragma unroll
+            for (int q = h * Q; q < (h + 1) * Q; ++q) {
+                bf16x8 b[CT];
+#pragma unroll
+                for (int c = 0; c < CT; ++c) b[c] = tokens(c, q);
+#pragma unroll
+                for (int r = 0; r <= R; ++r) {
+                    const bf16x8 a = r < R ? widen<FMT, G>(w[r < R ? r : 0], 1.0f, q) : ones;
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) d[r][c] = mfma(a, b[c], d[r][c]);
+                }
+            }
+            settle_all(d);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int at = i * G + h;
+                    const uint32_t sw = sc[r].s[at >> 1];
+                    const float sv = at & 1 ? bf16_hi(sw) : bf16_lo(sw);
+                    const uint32_t zw = sc[r].z[at >> 2] | 0x80808080u;          // 128 + zero
+                    const float z = (float)((zw >> (8 * (at & 3))) & 0xFFu);
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) acc[r][c][i] = fmaf(sv, fmaf(-z, d[R][c][i], d[r][c][i]), acc[r][c][i]);
+                }
+        }
+    } else {
+        uint32_t words[R];
+        if constexpr (F::kMx) spread_rows<R>(s.w, words);
+        f32x4 d[R][CT];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) d[r][c] = F::kMx ? acc[r][c] : none;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            bf16x8 b[CT];
+#pragma unroll
+            for (int c = 0; c < CT; ++c) b[c] = tokens(c, q);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float mx = 1.0f;
+                if constexpr (F::kMx) mx = e8m0_value(words[r], F::kFour ? g : 2 * (q >> 1) + (g >> 1));
+                const bf16x8 a = widen<FMT, G>(w[r], mx, q);
+#pragma unroll
+                for (int c = 0; c < CT; ++c) d[r][c] = mfma(a, b[c], d[r][c]);
+            }
+        }
+        settle_all(d);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                if constexpr (F::kMx) {
+                    acc[r][c] = d[r][c];
+                } else {
+                    const float sv = __uint_as_float(s.w);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[r][c][i] = fmaf(sv, d[r][c][i], acc[r][c][i]);
+                }
+            }
+    }
+}
+
+__device__ __forceinline__ void lds_barrier() {
+    // orders LDS accesses only: loads stay in flight across it
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // Token rows are read through a buffer resource: a lane whose column has no token passes kNoRow, which lies past

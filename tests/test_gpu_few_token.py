@@ -56,6 +56,27 @@ def test_matvec(fmt, group, z, m, n, k):
     check(got, xv @ exact[0].T, fp32_error(w, 0, xv, exact[0]), f"matvec {fmt} g{group} {m}x{n}x{k}")
 
 
+# wide matrices: more row tiles to a wavefront, and the form that shares tokens (65536 rows and more than 16 tokens)
+WIDE_SHAPES = [(1, 8200, 128), (6, 8192, 384), (13, 16388, 128), (16, 20000, 256), (24, 16400, 256), (40, 8204, 128),
+               (64, 16384, 256), (17, 65540, 128), (33, 65536, 384), (64, 65792, 256), (100, 65536, 128)]
+
+
+@pytest.mark.parametrize("fmt,group,z", FORMATS, ids=FORMAT_IDS)
+@pytest.mark.parametrize("m,n,k", WIDE_SHAPES)
+def test_matvec_of_many_rows(fmt, group, z, m, n, k):
+    require_gpu()
+    n = -(-n // 128) * 128 if fmt == "e4m3" else n
+    rng = np.random.default_rng(m + n + k)
+    w, exact = random_weight(rng, fmt, group, z, n, k)
+    x = activations(rng, m, k)
+    y = torch.full((m + 2, n), POISON, dtype=torch.int16, device="cuda")
+    moe.matvec(dev(x.view(np.int16)), to_gpu(w), out=y[1:m + 1])
+    xv = values(x)
+    check(values(host_u16(y[1:m + 1])), xv @ exact[0].T, fp32_error(w, 0, xv, exact[0]),
+          f"matvec {fmt} g{group} {m}x{n}x{k}")
+    assert (y[[0, m + 1]] == POISON).all()
+
+
 @pytest.mark.parametrize("fmt,group,z", FORMATS, ids=FORMAT_IDS)
 def test_matvec_picks_every_element(fmt, group, z):
     """x = unit vectors: y is column j of the weight, rounded once, for every j."""
@@ -185,7 +206,10 @@ def check_layer(c, got, what):
 LAYERS = [  # T, E, e0, L, k, H, I
     (1, 8, 0, 8, 2, 256, 128), (1, 16, 4, 8, 8, 128, 256), (2, 8, 0, 8, 1, 384, 128), (7, 64, 32, 32, 8, 256, 384),
     (16, 8, 0, 8, 3, 128, 128), (17, 40, 3, 33, 5, 256, 128), (33, 8, 0, 8, 2, 128, 256), (64, 8, 2, 5, 2, 256, 128),
-    (64, 300, 0, 300, 4, 128, 128), (65, 8, 0, 8, 2, 128, 128), (150, 16, 8, 8, 4, 128, 128)]
+    (64, 300, 0, 300, 4, 128, 128), (65, 8, 0, 8, 2, 128, 128), (150, 16, 8, 8, 4, 128, 128),
+    # many busy row tiles (two and four to a wavefront) and hidden sizes from 6144 (two in the down projection)
+    (8, 32, 0, 32, 8, 128, 384), (8, 32, 0, 32, 8, 128, 512), (30, 40, 0, 40, 4, 128, 512), (64, 64, 0, 64, 8, 128, 256),
+    (1, 2, 0, 2, 2, 6144, 128), (12, 2, 0, 2, 1, 6272, 128), (21, 3, 1, 2, 2, 6144, 128), (64, 2, 0, 2, 1, 6144, 128)]
 
 
 @pytest.mark.parametrize("fmt,group,z", FORMATS, ids=FORMAT_IDS)
@@ -218,6 +242,19 @@ def test_layer_odd_ids():
     got = run_layer(c)
     check_layer(c, got, "odd ids")
     assert not got[[0, 1, 5]].any()
+
+
+@pytest.mark.parametrize("fmt,group,z", FORMATS, ids=FORMAT_IDS)
+@pytest.mark.parametrize("E", [2, 64], ids=["E2", "E64"])
+def test_layer_every_token_names_one_expert(fmt, group, z, E):
+    """64 tokens for one expert, where 32 or 2 are expected: further passes over its weights."""
+    require_gpu()
+    c = make_layer(np.random.default_rng(E), 64, E, 0, 2, 1, 128, 256, (fmt, group, z))
+    c["ids"][:] = 1
+    check_layer(c, run_layer(c), f"one expert of {E}")
+    c["ids"][::3] = 0
+    c["ids"][5:9] = -1
+    check_layer(c, run_layer(c), f"two experts of {E}")
 
 
 def test_layer_nothing_local():
