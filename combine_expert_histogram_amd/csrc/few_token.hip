@@ -12,8 +12,11 @@ using namespace moe;
 
 constexpr int kWaves = 8;                  // wavefronts of a workgroup; they split the K blocks
 constexpr int kThreads = kWaves * MOE_WAVE;
-// K blocks a wavefront keeps in flight
-constexpr int depth_of(int R, int CT) { return CT > 1 || R == 4 ? 1 : R == 2 ? 2 : 4; }
+// K blocks a wavefront keeps in flight, and the wavefronts of a SIMD that its registers allow: two workgroups to a CU
+// hide each other's latencies (int4, groups of 128, 16 tokens: 99.7 -> 80.1 us for the gate and up products), which
+// one column tile allows unless an int4 format carries two or four scale groups a block (those would spill).
+constexpr int depth_of(int R, int CT, int XT) { return CT > 1 || R == 4 ? 1 : R == 2 || XT == 16 ? 2 : 4; }
+constexpr int waves_per_simd(int FMT, int G, int CT) { return CT == 1 && G == 1 ? 4 : 2; }
 constexpr int kChunk = 64;                 // tokens a layer launch handles: one lane each, four column tiles
 constexpr int kMaxTopK = 64;
 constexpr int kMaxLocal = 1024;
@@ -33,10 +36,11 @@ __device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
     *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 
-// acc += blocks [0, n) that load(step) brings, depth_of(R, CT) of them in flight; load returns block_product's cols.
-template <int FMT, int G, int R, int CT, int XT, class Load>
-__device__ __forceinline__ void stream_blocks(int n, Load&& load, u32x4* corner, f32x4 (&acc)[R][CT]) {
-    constexpr int kDepth = depth_of(R, CT);
+// acc += blocks [0, n) that load(step) brings, depth_of of them in flight; load returns block_product's cols, and done()
+// follows each block.
+template <int FMT, int G, int R, int CT, int XT, class Load, class Done>
+__device__ __forceinline__ void stream_blocks(int n, Load&& load, u32x4* corner, f32x4 (&acc)[R][CT], Done&& done) {
+    constexpr int kDepth = depth_of(R, CT, XT);
     Step<FMT, G, R, CT, XT> st[kDepth];
     uint32_t cols[kDepth];
 #pragma unroll
@@ -47,6 +51,7 @@ __device__ __forceinline__ void stream_blocks(int n, Load&& load, u32x4* corner,
         for (int u = 0; u < kDepth; ++u) {
             if (i + u < n) {
                 block_product<FMT, G, R, CT, XT>(st[u], cols[u], corner, acc);
+                done();
                 if (i + u + kDepth < n) cols[u] = load(st[u]);
             }
         }
@@ -55,7 +60,7 @@ __device__ __forceinline__ void stream_blocks(int n, Load&& load, u32x4* corner,
 
 // ---------------------------------------------------------------- y = x W^T
 template <int FMT, int G, int R, int CT, int XT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, waves_per_simd(FMT, G, CT))
 matvec_kernel(WView w, const uint16_t* __restrict__ x, int64_t ldx, int M, uint16_t* __restrict__ y, int64_t ldy) {
     __shared__ f32x4 red[kWaves][R * CT * 64];
     __shared__ u32x4 corner[kWaves][kCorner];
@@ -89,7 +94,7 @@ matvec_kernel(WView w, const uint16_t* __restrict__ x, int64_t ldx, int M, uint1
             if (CT == 1 || (cols >> c & 1)) load_rows<FMT, G, XT>(xb, xrow[c], kb, st.x[c]);
         ++kb;
         return cols;
-    }, corner[wave], acc);
+    }, corner[wave], acc, [] {});
 
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -199,12 +204,10 @@ struct LayerArgs {
     int T, k, e0, L, H, I;       // T <= kChunk
 };
 
-// The set of local experts that the tokens name, as bits in LDS (every thread calls; ends in a barrier).
-__device__ __forceinline__ void expert_set(const LayerArgs& a, uint32_t (&bits)[kMaxLocal / 32]) {
-    if (threadIdx.x < kMaxLocal / 32) bits[threadIdx.x] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.T * a.k; i += blockDim.x) {
-        const int64_t e = (int64_t)a.ids[i] - a.e0;
+// The set of local experts that the tokens name, as bits in LDS (cleared before; every thread calls; ends in a barrier).
+__device__ __forceinline__ void expert_set(const LayerArgs& a, const int32_t* ids, uint32_t (&bits)[kMaxLocal / 32]) {
+    for (int i = threadIdx.x; i < a.T * a.k; i += kThreads) {
+        const int64_t e = (int64_t)ids[i] - a.e0;
         if (e >= 0 && e < a.L) atomicOr(&bits[e >> 5], 1u << (e & 31));
     }
     __syncthreads();
@@ -227,13 +230,6 @@ __device__ __forceinline__ int nth_expert(const uint32_t (&bits)[kMaxLocal / 32]
     return word * 32 + __ffs(b) - 1;
 }
 
-__device__ __forceinline__ int next_expert(const uint32_t (&bits)[kMaxLocal / 32], int e) {
-    int word = e >> 5;
-    uint32_t b = __builtin_amdgcn_readfirstlane(bits[word]) & ~((2u << (e & 31)) - 1u);
-    while (b == 0 && ++word < kMaxLocal / 32) b = __builtin_amdgcn_readfirstlane(bits[word]);
-    return b ? word * 32 + __ffs(b) - 1 : -1;
-}
-
 template <int FMT, int G>
 __device__ __forceinline__ WView expert_view(const WView& w, int e) {
     using F = Fmt<FMT, G>;
@@ -251,38 +247,55 @@ __device__ __forceinline__ WView expert_view(const WView& w, int e) {
     return v;
 }
 
+// The tokens that name local expert e, as bits (lane t looks at token t's ids in LDS); first: this lane's first slot.
+__device__ __forceinline__ uint64_t tokens_of(const LayerArgs& a, const int32_t* ids, int e, int& first) {
+    const int t = lane_id();
+    first = -1;
+    if (t < a.T)
+        for (int j = a.k - 1; j >= 0; --j)
+            if (ids[t * a.k + j] == a.e0 + e) first = j;
+    return __ballot(first >= 0);
+}
+
 // First launch: h[t k + j] = w (silu(gate) up) in bf16, for the first slot j in which token t names the expert, w
 // the sum of the token's weights for it.  A workgroup takes 8 R columns of h of one expert: a tile's sixteen weight
 // rows are eight gate rows and the eight up rows that go with them.  The rounding of h to bf16 is the matrix
 // instruction's input type; it is of the size of the output's own.
 template <int FMT, int G, int R, int CT, int XT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, waves_per_simd(FMT, G, CT))
 gate_up_kernel(WView w, LayerArgs a) {
     __shared__ f32x4 red[kWaves][R * CT * 64];
     __shared__ u32x4 corner[kWaves][kCorner];
     __shared__ uint32_t bits[kMaxLocal / 32];
-    __shared__ int32_t tok[kChunk], slot[kChunk];
+    __shared__ int32_t tok[kWaves][kChunk], slot[kChunk];
     __shared__ float wt[kChunk];
-    expert_set(a, bits);
+    extern __shared__ int32_t ids[];         // [T * k], then the weights
+    float* const tw = reinterpret_cast<float*>(ids + a.T * a.k);
+    if (threadIdx.x < kMaxLocal / 32) bits[threadIdx.x] = 0;
+    for (int i = threadIdx.x; i < a.T * a.k; i += kThreads) {
+        ids[i] = a.ids[i];
+        tw[i] = a.topk_w[i];
+    }
+    __syncthreads();
+    expert_set(a, ids, bits);
     if ((int)blockIdx.y >= expert_count(bits)) return;
     const int e = nth_expert(bits, blockIdx.y);
     const int lane = lane_id(), wave = wave_index();
 
-    int first = -1;                          // lane t: the slot of token t
-    float sum = 0.f;
-    if (lane < a.T)
-        for (int j = a.k - 1; j >= 0; --j)
-            if (a.ids[lane * a.k + j] == a.e0 + e) first = j;
-    if (first >= 0)
-        for (int j = first; j < a.k; ++j)
-            if (a.ids[lane * a.k + j] == a.e0 + e) sum += a.topk_w[lane * a.k + j];
-    const uint64_t here = __ballot(first >= 0);
+    int first;
+    const uint64_t here = tokens_of(a, ids, e, first);
     const int ncols = __popcll(here);
-    if (wave == 0 && first >= 0) {
+    if (first >= 0) {                        // each wavefront its own list: no barrier before the stream
         const int at = __popcll(here & lanemask_lt());
-        tok[at] = lane, slot[at] = lane * a.k + first, wt[at] = sum;
+        tok[wave][at] = lane;
+        if (wave == 0) {
+            float sum = 0.f;
+            for (int j = first; j < a.k; ++j)
+                if (ids[lane * a.k + j] == a.e0 + e) sum += tw[lane * a.k + j];
+            slot[at] = lane * a.k + first, wt[at] = sum;
+        }
     }
-    __syncthreads();
+    __builtin_amdgcn_wave_barrier();         // one wavefront's LDS accesses stay in order
 
     const WView v = expert_view<FMT, G>(w, e);
     const int i0 = blockIdx.x * (8 * R);
@@ -297,7 +310,7 @@ gate_up_kernel(WView w, LayerArgs a) {
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
             const int t = col0 + XT * c + token_of_lane<XT>();
-            xrow[c] = t < ncols ? (uint32_t)(tok[t] * a.H * 2) : kNoRow;
+            xrow[c] = t < ncols ? (uint32_t)(tok[wave][t] * a.H * 2) : kNoRow;
             if (col0 + XT * c < ncols) cols |= 1u << c;
         }
 
@@ -311,7 +324,7 @@ gate_up_kernel(WView w, LayerArgs a) {
                 if (CT == 1 || (cols >> c & 1)) load_rows<FMT, G, XT>(xb, xrow[c], kb, st.x[c]);
             ++kb;
             return cols;
-        }, corner[wave], acc);
+        }, corner[wave], acc, [] {});
 
         if (col0 > 0) __syncthreads();       // the sums of the pass before are read
 #pragma unroll
@@ -333,73 +346,128 @@ gate_up_kernel(WView w, LayerArgs a) {
     }
 }
 
-// Second launch: out[t] = sum over the experts of W2[e] h[t, e], one long product whose K runs over the experts
-// hit.  The sixteen columns are the tokens themselves (a token that does not name the expert reads zeros), so the
-// sum over experts stays in the accumulators and its order is fixed.
-template <int FMT, int G, int R, int CT, int XT>
-__global__ void __launch_bounds__(kThreads)
+// The passes over the experts' weights that the tokens need, XT tokens each, in the experts' order: segs[i] holds expert
+// and pass.  A token that names an expert twice counts twice and may leave a pass without tokens.  Every thread calls;
+// ends in a barrier.  Returns their number.
+constexpr uint32_t seg_expert(uint32_t s) { return s & 0xFFFFu; }
+constexpr uint32_t seg_pass(uint32_t s) { return s >> 16; }
+
+template <int XT>
+__device__ __forceinline__ int list_passes(const LayerArgs& a, const int32_t* ids, uint32_t* segs) {
+    __shared__ int32_t count[kMaxLocal];
+    __shared__ int32_t before[kWaves];
+    static_assert(kMaxLocal == 2 * kThreads, "two experts to a thread");
+    const int tid = threadIdx.x, wave = wave_index();
+    count[2 * tid] = count[2 * tid + 1] = 0;
+    __syncthreads();
+    for (int i = tid; i < a.T * a.k; i += kThreads) {
+        const int64_t e = (int64_t)ids[i] - a.e0;
+        if (e >= 0 && e < a.L) atomicAdd(&count[e], 1);
+    }
+    __syncthreads();
+    const int p0 = (count[2 * tid] + XT - 1) / XT, p1 = (count[2 * tid + 1] + XT - 1) / XT;
+    const int upto = wave_inclusive_scan(p0 + p1);
+    if (lane_id() == MOE_WAVE - 1) before[wave] = upto;
+    __syncthreads();
+    int at = upto - p0 - p1, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        if (w < wave) at += before[w];
+        total += before[w];
+    }
+    for (int p = 0; p < p0; ++p) segs[at++] = (uint32_t)(2 * tid) | (uint32_t)p << 16;
+    for (int p = 0; p < p1; ++p) segs[at++] = (uint32_t)(2 * tid + 1) | (uint32_t)p << 16;
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(total);
+}
+
+// Second launch: out[t] = sum over the experts of W2[e] h[t, e], one long product whose K runs over the experts hit
+// (each wavefront takes a run of it).  An expert's tokens sit in compact columns, so that the few tokens that an
+// expert has take few loads; at the expert's end their sums move to the columns of the tokens (a lane permutation
+// within the wavefront), which keeps the sum over experts in registers and its order fixed.  OT tiles of 16 tokens.
+template <int FMT, int G, int R, int XT, int OT>
+__global__ void __launch_bounds__(kThreads, waves_per_simd(FMT, G, OT > 2 ? OT : 1))
 down_kernel(WView w, LayerArgs a) {
-    __shared__ f32x4 red[kWaves][R * CT * 64];
+    __shared__ f32x4 red[kWaves][R * OT * 64];
     __shared__ u32x4 corner[kWaves][kCorner];
-    __shared__ uint32_t bits[kMaxLocal / 32];
-    extern __shared__ int32_t ids[];         // [T * k]
+    __shared__ int32_t rows[kWaves][kChunk];
+    extern __shared__ int32_t ids[];         // [T * k], then as many passes
+    uint32_t* const segs = reinterpret_cast<uint32_t*>(ids + a.T * a.k);
     for (int i = threadIdx.x; i < a.T * a.k; i += kThreads) ids[i] = a.ids[i];
-    expert_set(a, bits);
-    const int lane = lane_id(), wave = wave_index();
+    __syncthreads();
+    const int64_t total = (int64_t)list_passes<XT>(a, ids, segs) * w.nb;
+    const int lane = lane_id(), wave = wave_index(), g = lane >> 4;
     const int row0 = blockIdx.x * (16 * R);
-    const int64_t total = (int64_t)expert_count(bits) * w.nb;
-    const int f0 = (int)(total * wave / kWaves);
-    const int n = (int)(total * (wave + 1) / kWaves) - f0;
+    const int64_t f0 = total * wave / kWaves;
+    const int n = (int)(total * (wave + 1) / kWaves - f0);
 
     const __amdgpu_buffer_rsrc_t hb = row_buffer(a.h, (uint32_t)(a.T * a.k * a.I * 2));
-    int e = 0, kb = 0;
+    int seg = (int)(f0 / w.nb), kb = (int)(f0 % w.nb);       // of the next block to load
+    int done_seg = seg, done_kb = kb;                        // of the next one to finish
     WView v = w;
     Tiles<FMT, G, R> tiles;
-    uint32_t hrow[CT];
-    uint32_t cols = 0;
-    auto enter = [&](int expert) {           // this lane's rows and columns of an expert
-        e = expert;
-        v = expert_view<FMT, G>(w, e);
+    uint32_t hrow[1];
+    const auto enter = [&] {                 // this lane's rows and column of a pass
+        const uint32_t s = __builtin_amdgcn_readfirstlane(segs[seg]);
+        v = expert_view<FMT, G>(w, seg_expert(s));
         tiles = tiles_of<FMT, G, R>(
             v, [&](int t, int i) { return row0 + 16 * t + i; }, [&](int t, int i) { return row0 + 16 * t + 4 * i; });
-        cols = 0;
-#pragma unroll
-        for (int c = 0; c < CT; ++c) {
-            const int t = XT * c + token_of_lane<XT>();
-            hrow[c] = kNoRow;
-            if (t < a.T)
-                for (int j = a.k - 1; j >= 0; --j)
-                    if (ids[t * a.k + j] == a.e0 + e) hrow[c] = (uint32_t)((t * a.k + j) * a.I * 2);
-            if (__ballot(hrow[c] != kNoRow)) cols |= 1u << c;
-        }
+        int first;
+        const uint64_t here = tokens_of(a, ids, seg_expert(s), first);
+        if (first >= 0) rows[wave][__popcll(here & lanemask_lt())] = lane * a.k + first;
+        __builtin_amdgcn_wave_barrier();     // one wavefront's LDS accesses stay in order
+        const int c = (int)seg_pass(s) * XT + token_of_lane<XT>();
+        hrow[0] = c < __popcll(here) ? (uint32_t)(rows[wave][c] * a.I * 2) : kNoRow;
     };
-    if (n > 0) {
-        kb = f0 % w.nb;
-        enter(nth_expert(bits, f0 / w.nb));
-    }
-    f32x4 acc[R][CT] = {};
-    stream_blocks<FMT, G, R, CT, XT>(n, [&](Step<FMT, G, R, CT, XT>& st) {
+    f32x4 acc[R][1] = {}, out[R][OT] = {};
+    const auto leave = [&] {                 // the pass's columns to the tokens'
+        const uint32_t s = __builtin_amdgcn_readfirstlane(segs[done_seg]);
+        int first;
+        const uint64_t here = tokens_of(a, ids, seg_expert(s), first);
+#pragma unroll
+        for (int o = 0; o < OT; ++o) {
+            if (OT > 1 && (here >> (16 * o) & 0xFFFFu) == 0) continue;
+            const int t = 16 * o + (lane & 15);
+            const int c = __popcll(here & ((1ull << t) - 1)) - (int)seg_pass(s) * XT;
+            const bool mine = (here >> t & 1) && c >= 0 && c < XT;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float f = __shfl(acc[r][0][i], c * (16 / XT) + 16 * g, MOE_WAVE);
+                    out[r][o][i] += mine ? f : 0.f;
+                }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[r][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+    };
+    if (n > 0) enter();
+    stream_blocks<FMT, G, R, 1, XT>(n, [&](Step<FMT, G, R, 1, XT>& st) {
         if (kb == w.nb) {
             kb = 0;
-            enter(next_expert(bits, e));
+            ++seg;
+            enter();
         }
         load_weights<FMT, G, R>(tiles, v, kb, st.w, st.s);
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-            if (CT == 1 || (cols >> c & 1)) load_rows<FMT, G, XT>(hb, hrow[c], kb, st.x[c]);
+        load_rows<FMT, G, XT>(hb, hrow[0], kb, st.x[0]);
         ++kb;
-        return cols;
-    }, corner[wave], acc);
+        return 1u;
+    }, corner[wave], acc, [&] {
+        if (++done_kb < w.nb) return;
+        leave();
+        done_kb = 0;
+        ++done_seg;
+    });
+    if (n > 0 && done_kb > 0) leave();
 
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int c = 0; c < CT; ++c) red[wave][(r * CT + c) * 64 + lane] = acc[r][c];
+        for (int o = 0; o < OT; ++o) red[wave][(r * OT + o) * 64 + lane] = out[r][o];
     __syncthreads();
-    for (int at = threadIdx.x; at < R * CT * 64; at += kThreads) {
-        const int r = at / (64 * CT), c = at / 64 % CT, l = at & 63;
-        const int t = XT * c + (l & 15) / (16 / XT);
-        if ((l & 15) % (16 / XT)) continue;              // a repeated column
+    for (int at = threadIdx.x; at < R * OT * 64; at += kThreads) {
+        const int r = at / (64 * OT), o = at / 64 % OT, l = at & 63;
+        const int t = 16 * o + (l & 15);
         if (t < a.T) store4(a.out + (int64_t)t * a.H + row0 + 16 * r + 4 * (l >> 4), sum_waves(red, at));
     }
 }
@@ -560,18 +628,20 @@ extern "C" moe_status moe_few_token_layer(const moe_dims* dims, int32_t inter, c
         a.out = out_bf16 + t0 * d.H;
         a.T = (int)std::min<int64_t>(d.T - t0, kChunk);
         a.k = (int)d.k, a.e0 = (int)d.e0, a.L = (int)d.L, a.H = (int)d.H, a.I = inter;
-        // columns for twice the tokens that an expert can expect; an expert with more takes another pass
-        const int64_t share = a.T <= 16 ? a.T : std::min<int64_t>(std::max<int64_t>(2 * a.T * d.k / d.E, 9), 32);
+        // columns for the tokens that an expert of uniform routing has, and two deviations more: an expert with more
+        // takes a further pass
+        const double mean = (double)a.T * d.k / d.E;
+        const int64_t share = std::min<int64_t>(a.T, (int64_t)std::ceil(mean + 2.0 * std::sqrt(mean)));
         // workgroups of one row tile that uniform routing would keep busy
         const double hit = d.L * (1.0 - std::pow(1.0 - (double)d.k / d.E, (double)a.T));
         const int64_t busy = (int64_t)(hit * (inter / 8));
         const int r1 = busy >= 4 * kCus ? 4 : busy >= 2 * kCus ? 2 : 1;
         st = with_format(w1->format, g1, [&](auto fmt, auto g) {
-            with_cols(share, [&](auto ct, auto xt) {
+            with_cols(std::min<int64_t>(share, 32), [&](auto ct, auto xt) {
                 if constexpr (ct <= 2)
                     with_rows<1, 2, 4>(r1, [&](auto r) {
                         const dim3 grid((unsigned)(inter / (8 * r)), (unsigned)std::min<int64_t>(a.T * d.k, d.L));
-                        gate_up_kernel<fmt, g, r, ct, xt><<<grid, kThreads, 0, stream>>>(v1, a);
+                        gate_up_kernel<fmt, g, r, ct, xt><<<grid, kThreads, a.T * a.k * 8, stream>>>(v1, a);
                     });
             });
             return launch_status();
@@ -579,11 +649,14 @@ extern "C" moe_status moe_few_token_layer(const moe_dims* dims, int32_t inter, c
         if (st != MOE_OK) return st;
         const int r2 = d.H >= 24 * kCus ? 2 : 1;
         st = with_format(w2->format, g2, [&](auto fmt, auto g) {
-            with_cols(a.T, [&](auto ct, auto xt) {
-                with_rows<1, 2>(r2, [&](auto r) {
-                    down_kernel<fmt, g, r, ct, xt><<<dim3((unsigned)(d.H / (16 * r))), kThreads, a.T * a.k * 4, stream>>>(
-                        v2, a);
-                });
+            with_cols(std::min<int64_t>(share, 16), [&](auto ct, auto xt) {
+                if constexpr (ct == 1)
+                    with_rows<1, 2>(r2, [&](auto r) {
+                        with_rows<1, 2, 4>(a.T <= 16 ? 1 : a.T <= 32 ? 2 : 4, [&](auto ot) {
+                            down_kernel<fmt, g, r, xt, ot>
+                                <<<dim3((unsigned)(d.H / (16 * r))), kThreads, a.T * a.k * 8, stream>>>(v2, a);
+                        });
+                    });
             });
             return launch_status();
         });

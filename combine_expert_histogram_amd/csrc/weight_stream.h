@@ -186,6 +186,13 @@ __device__ __forceinline__ uint32_t row_lane(uint32_t w) {
     return (uint32_t)__builtin_amdgcn_mov_dpp((int)w, 0x150 + T, 0xF, 0xF, false);    // row_newbcast
 }
 
+// ... of tile r (a constant after unrolling)
+template <int R>
+__device__ __forceinline__ uint32_t tile_word(uint32_t w, int r) {
+    if constexpr (R == 1) return w;
+    return r == 0 ? row_lane<0>(w) : r == 1 ? row_lane<1>(w) : r == 2 ? row_lane<2>(w) : row_lane<3>(w);
+}
+
 template <int G, int R, int T = 0>
 __device__ __forceinline__ void spread_lanes(const Scales<MOE_W_INT4, G>& s, Scales<MOE_W_INT4, G> (&o)[R]) {
     if constexpr (R == 1) {
@@ -315,7 +322,57 @@ __device__ __forceinline__ void block_product(Step<FMT, G, R, CT, XT>& st, uint3
     turn_weights<FMT, G, R>(corner, st.w);
     const int g = lane_id() >> 4;
     const f32x4 none = {0.f, 0.f, 0.f, 0.f};
-    if constexpr (F::kInt4) {
+    if constexpr (CT == 1 && G == 1) {
+        // two tiles at a time, widened where they are used: what is live at once decides the wavefronts of a CU
+        constexpr int TG = R < 2 ? R : 2;
+        const u32x4 ones_bits = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+        uint32_t words[R];
+        if constexpr (F::kMx) spread_rows<R>(st.s.w, words);
+        f32x4 sum[1] = {none};
+        if constexpr (F::kInt4) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                sum[0] = mfma(__builtin_bit_cast(bf16x8, ones_bits), token_values<XT>(st.x[0], q), sum[0]);
+            settle(sum);
+        }
+#pragma unroll
+        for (int r0 = 0; r0 < R; r0 += TG) {
+            f32x4 d[TG];
+#pragma unroll
+            for (int r = 0; r < TG; ++r) d[r] = F::kMx ? acc[r0 + r][0] : none;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const bf16x8 b = token_values<XT>(st.x[0], q);
+#pragma unroll
+                for (int r = 0; r < TG; ++r) {
+                    float mx = 1.0f;
+                    if constexpr (F::kMx) mx = e8m0_value(words[r0 + r], F::kFour ? g : 2 * (q >> 1) + (g >> 1));
+                    d[r] = mfma(widen<FMT, G>(st.w[r0 + r], mx, q), b, d[r]);
+                }
+            }
+            settle(d);
+#pragma unroll
+            for (int r = 0; r < TG; ++r) {
+                if constexpr (F::kMx) {
+                    acc[r0 + r][0] = d[r];
+                } else if constexpr (F::kInt4) {
+                    // sum (q - z) s x = s (sum (128 + q) x - (128 + z) sum x)
+                    const uint32_t zw = tile_word<R>(st.s.z[0], r0 + r) | 0x80808080u;       // 128 + zero
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t sw = tile_word<R>(st.s.s[i >> 1], r0 + r);
+                        const float s = i & 1 ? bf16_hi(sw) : bf16_lo(sw);
+                        const float z = (float)((zw >> (8 * i)) & 0xFFu);
+                        acc[r0 + r][0][i] = fmaf(s, fmaf(-z, sum[0][i], d[r][i]), acc[r0 + r][0][i]);
+                    }
+                } else {
+                    const float s = __uint_as_float(st.s.w);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[r0 + r][0][i] = fmaf(s, d[r][i], acc[r0 + r][0][i]);
+                }
+            }
+        }
+    } else if constexpr (F::kInt4) {
         // sum (q - z) s x = s (sum (128 + q) x - (128 + z) sum x) per scale group; sum x from an MFMA by ones
         const u32x4 ones_bits = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
         const bf16x8 ones = __builtin_bit_cast(bf16x8, ones_bits);
