@@ -24,11 +24,11 @@ constexpr int kMaxLocal = 1024;
 __device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane(threadIdx.x / MOE_WAVE); }
 
 // Sums the wavefronts' partial tiles (fixed order): element at (r * CT + c, lane).
-template <int N>
-__device__ __forceinline__ f32x4 sum_waves(const f32x4 (&red)[kWaves][N], int at) {
+template <int NW, int N>
+__device__ __forceinline__ f32x4 sum_waves(const f32x4 (&red)[NW][N], int at) {
     f32x4 s = red[0][at];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) s += red[w][at];
+    for (int w = 1; w < NW; ++w) s += red[w][at];
     return s;
 }
 
@@ -352,54 +352,63 @@ gate_up_kernel(WView w, LayerArgs a) {
 constexpr uint32_t seg_expert(uint32_t s) { return s & 0xFFFFu; }
 constexpr uint32_t seg_pass(uint32_t s) { return s >> 16; }
 
-template <int XT>
+template <int XT, int NW>
 __device__ __forceinline__ int list_passes(const LayerArgs& a, const int32_t* ids, uint32_t* segs) {
     __shared__ int32_t count[kMaxLocal];
-    __shared__ int32_t before[kWaves];
-    static_assert(kMaxLocal == 2 * kThreads, "two experts to a thread");
+    __shared__ int32_t before[NW];
+    constexpr int kMine = kMaxLocal / (NW * MOE_WAVE);       // experts of a thread
     const int tid = threadIdx.x, wave = wave_index();
-    count[2 * tid] = count[2 * tid + 1] = 0;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) count[kMine * tid + i] = 0;
     __syncthreads();
-    for (int i = tid; i < a.T * a.k; i += kThreads) {
+    for (int i = tid; i < a.T * a.k; i += NW * MOE_WAVE) {
         const int64_t e = (int64_t)ids[i] - a.e0;
         if (e >= 0 && e < a.L) atomicAdd(&count[e], 1);
     }
     __syncthreads();
-    const int p0 = (count[2 * tid] + XT - 1) / XT, p1 = (count[2 * tid + 1] + XT - 1) / XT;
-    const int upto = wave_inclusive_scan(p0 + p1);
+    int passes[kMine], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) mine += passes[i] = (count[kMine * tid + i] + XT - 1) / XT;
+    const int upto = wave_inclusive_scan(mine);
     if (lane_id() == MOE_WAVE - 1) before[wave] = upto;
     __syncthreads();
-    int at = upto - p0 - p1, total = 0;
+    int at = upto - mine, total = 0;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < NW; ++w) {
         if (w < wave) at += before[w];
         total += before[w];
     }
-    for (int p = 0; p < p0; ++p) segs[at++] = (uint32_t)(2 * tid) | (uint32_t)p << 16;
-    for (int p = 0; p < p1; ++p) segs[at++] = (uint32_t)(2 * tid + 1) | (uint32_t)p << 16;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+        for (int p = 0; p < passes[i]; ++p) segs[at++] = (uint32_t)(kMine * tid + i) | (uint32_t)p << 16;
     __syncthreads();
     return __builtin_amdgcn_readfirstlane(total);
 }
+
+// Wavefronts of a down workgroup.  One row tile is taken where the rows give every CU only one workgroup, which then
+// needs sixteen to hide a block's latency (4096 rows, int4, 16 tokens: 52.4 us with eight, 42.4 with sixteen; with two
+// row tiles both take the same); more scale groups would spill and four output tiles would not fit LDS.
+constexpr int down_waves(int G, int R, int OT) { return R == 1 && OT <= 2 && G == 1 ? 16 : 8; }
 
 // Second launch: out[t] = sum over the experts of W2[e] h[t, e], one long product whose K runs over the experts hit
 // (each wavefront takes a run of it).  An expert's tokens sit in compact columns, so that the few tokens that an
 // expert has take few loads; at the expert's end their sums move to the columns of the tokens (a lane permutation
 // within the wavefront), which keeps the sum over experts in registers and its order fixed.  OT tiles of 16 tokens.
-template <int FMT, int G, int R, int XT, int OT>
-__global__ void __launch_bounds__(kThreads, waves_per_simd(FMT, G, OT > 2 ? OT : 1))
+template <int FMT, int G, int R, int XT, int OT, int NW>
+__global__ void __launch_bounds__(NW * MOE_WAVE, waves_per_simd(FMT, G, OT > 2 ? OT : 1))
 down_kernel(WView w, LayerArgs a) {
-    __shared__ f32x4 red[kWaves][R * OT * 64];
-    __shared__ u32x4 corner[kWaves][kCorner];
-    __shared__ int32_t rows[kWaves][kChunk];
+    __shared__ f32x4 red[NW][R * OT * 64];
+    __shared__ u32x4 corner[NW][kCorner];
+    __shared__ int32_t rows[NW][kChunk];
     extern __shared__ int32_t ids[];         // [T * k], then as many passes
     uint32_t* const segs = reinterpret_cast<uint32_t*>(ids + a.T * a.k);
-    for (int i = threadIdx.x; i < a.T * a.k; i += kThreads) ids[i] = a.ids[i];
+    for (int i = threadIdx.x; i < a.T * a.k; i += NW * MOE_WAVE) ids[i] = a.ids[i];
     __syncthreads();
-    const int64_t total = (int64_t)list_passes<XT>(a, ids, segs) * w.nb;
+    const int64_t total = (int64_t)list_passes<XT, NW>(a, ids, segs) * w.nb;
     const int lane = lane_id(), wave = wave_index(), g = lane >> 4;
     const int row0 = blockIdx.x * (16 * R);
-    const int64_t f0 = total * wave / kWaves;
-    const int n = (int)(total * (wave + 1) / kWaves - f0);
+    const int64_t f0 = total * wave / NW;
+    const int n = (int)(total * (wave + 1) / NW - f0);
 
     const __amdgpu_buffer_rsrc_t hb = row_buffer(a.h, (uint32_t)(a.T * a.k * a.I * 2));
     int seg = (int)(f0 / w.nb), kb = (int)(f0 % w.nb);       // of the next block to load
@@ -465,7 +474,7 @@ down_kernel(WView w, LayerArgs a) {
 #pragma unroll
         for (int o = 0; o < OT; ++o) red[wave][(r * OT + o) * 64 + lane] = out[r][o];
     __syncthreads();
-    for (int at = threadIdx.x; at < R * OT * 64; at += kThreads) {
+    for (int at = threadIdx.x; at < R * OT * 64; at += NW * MOE_WAVE) {
         const int r = at / (64 * OT), o = at / 64 % OT, l = at & 63;
         const int t = 16 * o + (l & 15);
         if (t < a.T) store4(a.out + (int64_t)t * a.H + row0 + 16 * r + 4 * (l >> 4), sum_waves(red, at));
@@ -653,8 +662,9 @@ extern "C" moe_status moe_few_token_layer(const moe_dims* dims, int32_t inter, c
                 if constexpr (ct == 1)
                     with_rows<1, 2>(r2, [&](auto r) {
                         with_rows<1, 2, 4>(a.T <= 16 ? 1 : a.T <= 32 ? 2 : 4, [&](auto ot) {
-                            down_kernel<fmt, g, r, xt, ot>
-                                <<<dim3((unsigned)(d.H / (16 * r))), kThreads, a.T * a.k * 8, stream>>>(v2, a);
+                            constexpr int NW = down_waves(g, r, ot);
+                            down_kernel<fmt, g, r, xt, ot, NW>
+                                <<<dim3((unsigned)(d.H / (16 * r))), NW * MOE_WAVE, a.T * a.k * 8, stream>>>(v2, a);
                         });
                     });
             });
