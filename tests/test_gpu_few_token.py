@@ -257,6 +257,26 @@ def test_layer_every_token_names_one_expert(fmt, group, z, E):
     check_layer(c, run_layer(c), f"two experts of {E}")
 
 
+@pytest.mark.parametrize("f", [0, 2, 4], ids=lambda f: FORMAT_IDS[f])
+@pytest.mark.parametrize("shape", [(64, 64, 0, 64, 64, 128, 128), (64, 64, 3, 2, 64, 6144, 128), (64, 64, 3, 2, 64, 128, 128),
+                                   (32, 64, 3, 2, 64, 128, 128), (16, 1024, 0, 1024, 64, 128, 128)],
+                         ids=lambda s: "T%d_E%d_e%d_L%d_k%d_H%d_I%d" % s)
+def test_layer_at_the_largest_top_k(f, shape):
+    require_gpu()
+    c = make_layer(np.random.default_rng(sum(shape)), *shape, FORMATS[f])
+    check_layer(c, run_layer(c), f"top-64 {FORMATS[f]} {shape}")
+
+
+@pytest.mark.parametrize("T,k", [(1, 64), (17, 5), (64, 64)])
+def test_layer_one_expert_in_every_slot(T, k):
+    """Every slot of every token names the same expert: one product a token, with the summed weights."""
+    require_gpu()
+    c = make_layer(np.random.default_rng(T), T, 64, 5, 3, k, 128, 128, FORMATS[2])
+    c["ids"][:] = 6
+    c["tw"] /= k
+    check_layer(c, run_layer(c), f"T={T} k={k}")
+
+
 def test_layer_nothing_local():
     require_gpu()
     c = make_layer(np.random.default_rng(2), 40, 16, 4, 8, 4, 128, 128, FORMATS[2])
