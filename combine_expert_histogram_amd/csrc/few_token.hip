@@ -395,7 +395,7 @@ constexpr int down_waves(int G, int R, int OT) { return R == 1 && OT <= 2 && G =
 // expert has take few loads; at the expert's end their sums move to the columns of the tokens (a lane permutation
 // within the wavefront), which keeps the sum over experts in registers and its order fixed.  OT tiles of 16 tokens.
 template <int FMT, int G, int R, int XT, int OT, int NW>
-__global__ void __launch_bounds__(NW * MOE_WAVE, waves_per_simd(FMT, G, OT > 2 ? OT : 1))
+__global__ void __launch_bounds__(NW * MOE_WAVE, waves_per_simd(FMT, G, OT > 2 || OT * XT > 16 ? OT : 1))
 down_kernel(WView w, LayerArgs a) {
     __shared__ f32x4 red[NW][R * OT * 64];
     __shared__ u32x4 corner[NW][kCorner];
@@ -541,14 +541,18 @@ void with_rows(int r, F&& f) {
 
 constexpr int kCus = 256;
 
-// Row tiles of a wavefront of the wide product, and whether it pays: its workgroups take 256 rows each and need most
-// of the CUs, while the plain form's token traffic grows with the column tiles (the figures are beside moe_matvec).
+// Row tiles of a wavefront of the wide product, and whether it pays: its workgroups take 256 rows each and want every
+// CU, while the plain form's token traffic grows with the column tiles.  us, plain form (four row tiles) / wide form:
+//   e2m1, K = 7168, 64 tokens: 16384 rows 29 / 68, 32768 rows 58 (twice that) / 70, 131072 rows 234 / 140
+//   e2m1, K = 7168, 24 to 32 tokens: 16384 rows 21 / 58, 131072 rows 166 / 110;  e4m3, 64 tokens: 16384 rows 39 / 89
+// With four row tiles the wide form has half the LDS reads but one workgroup a CU, and takes the same (145 us).
 constexpr int kWideRows = 2;
 constexpr int64_t kWideGroupRows = kWaves * 16 * kWideRows;
 bool wide_pays(int64_t n, int64_t m) { return m > 16 && n >= kCus * kWideGroupRows; }
 
 // Row tiles of a wavefront: the more, the fewer token loads a weight load takes beside it, as long as there is a
-// workgroup for every CU.
+// workgroup for every CU.  us with 1 / 2 / 4 of them (e2m1): 4096 x 7168, 1 token: 6.2 / 7.5 / 11.6; 16384 x 4096, 16
+// tokens: - / 12.5 / 11.2; 131072 x 7168, 16 tokens: - / 140 / 115.
 int matvec_rows(int64_t n) {
     int r = 1;
     while (r < 4 && n >= 16 * 2 * r * kCus) r *= 2;
@@ -567,8 +571,8 @@ extern "C" moe_status moe_matvec(int32_t m, int32_t n, int32_t k, const uint16_t
     if (m == 0) return MOE_OK;
     if (!x_bf16 || !y_bf16 || !aligned(x_bf16, 16) || !aligned(y_bf16, 8)) return MOE_ERR_INVALID_ARG;
     if (x_stride < k || x_stride % 8 != 0 || y_stride < n || y_stride % 4 != 0) return MOE_ERR_INVALID_ARG;
-    // a workgroup's token rows are addressed with 31-bit byte offsets
-    if (x_stride >= (1 << 24)) return MOE_ERR_UNSUPPORTED;
+    // a workgroup's token rows are addressed with 31-bit byte offsets; the rest keeps the grid within its limits
+    if (x_stride >= (1 << 24) || m > (1 << 20) || n > (1 << 27)) return MOE_ERR_UNSUPPORTED;
     hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
     return with_format(w->format, groups, [&](auto fmt, auto g) {
         if (wide_pays(n, m)) {
@@ -599,7 +603,7 @@ extern "C" moe_status moe_few_token_layer_workspace(const moe_dims* dims, int32_
     moe_status st = load_dims(dims, &d, true);
     if (st != MOE_OK) return st;
     if (!bytes || inter < 128 || inter % 128 != 0) return MOE_ERR_INVALID_ARG;
-    if (d.L > kMaxLocal || d.k > kMaxTopK) return MOE_ERR_UNSUPPORTED;
+    if (d.L > kMaxLocal || d.k > kMaxTopK || inter >= (1 << 24)) return MOE_ERR_UNSUPPORTED;
     *bytes = (size_t)(std::min<int64_t>(d.T, kChunk) * d.k * inter * 2 + 255) / 256 * 256;
     return MOE_OK;
 }
@@ -641,7 +645,8 @@ extern "C" moe_status moe_few_token_layer(const moe_dims* dims, int32_t inter, c
         // takes a further pass
         const double mean = (double)a.T * d.k / d.E;
         const int64_t share = std::min<int64_t>(a.T, (int64_t)std::ceil(mean + 2.0 * std::sqrt(mean)));
-        // workgroups of one row tile that uniform routing would keep busy
+        // workgroups of one row tile that uniform routing would keep busy: 1 / 2 / 4 tiles by the rule of moe_matvec
+        // (one token, e2m1, 2048 workgroups: 43.0 / 29.2 / 28.2 us)
         const double hit = d.L * (1.0 - std::pow(1.0 - (double)d.k / d.E, (double)a.T));
         const int64_t busy = (int64_t)(hit * (inter / 8));
         const int r1 = busy >= 4 * kCus ? 4 : busy >= 2 * kCus ? 2 : 1;
@@ -656,6 +661,8 @@ extern "C" moe_status moe_few_token_layer(const moe_dims* dims, int32_t inter, c
             return launch_status();
         });
         if (st != MOE_OK) return st;
+        // two row tiles from three quarters of a workgroup a CU: 7168 rows 17.3 us against 22.4 with one (one token,
+        // e2m1); 4096 rows 67 against 57 (16 tokens, int4)
         const int r2 = d.H >= 24 * kCus ? 2 : 1;
         st = with_format(w2->format, g2, [&](auto fmt, auto g) {
             with_cols(std::min<int64_t>(share, 16), [&](auto ct, auto xt) {

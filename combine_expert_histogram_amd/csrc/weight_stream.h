@@ -7,7 +7,12 @@
 // tokens as its B operand (column l % 16), so a lane's four results are four consecutive weight rows of one token.
 // Every weight format widens to bf16 without rounding (an e4m3 or e2m1 code times a power of two; an integer
 // 128 + q), so the products are those of the definition and the sums are fp32.  One token uses one column of the
-// sixteen: the loop is bound by the weight stream up to 64 columns, not by the matrix cores.
+// sixteen: with 4-bit weights the matrix cores take 16 cycles of a CU for a KiB and column tile, the weight stream 90
+// (at 7 TB/s), so up to 64 tokens the stream is the floor.  What it comes to on one MI355X, us and TB/s of weights:
+//   131072 x 7168 e2m1: 1 token 92 (5.4), 16 tokens 115 (4.4), 64 tokens 140 (3.7)
+//   65536 x 7168 e4m3:  1 token 78 (6.0), 16 tokens 85 (5.6), 64 tokens 109 (4.4)
+//   131072 x 7168 int4, 1 token: groups of 128 98 (5.0), of 32 145 (3.9: vector instructions, 16 scales a row tile's
+//   block and lane to convert and apply)
 //
 // Which k a lane holds is free as long as both operands agree.  A lane always loads 16 B of one weight row, four
 // lanes cover 64 B of it, and the K order of the MFMAs follows from that:
@@ -22,7 +27,6 @@
 namespace moe {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
@@ -48,7 +52,7 @@ struct Fmt {
 };
 
 // The scales of R tiles and one block, one load for all of them: the sixteen lanes that would repeat one tile's
-// scales fetch other tiles' instead, and tile_scales hands them round.
+// scales fetch other tiles' instead, and spread_rows or row_lane hands them round.
 //   e4m3: the R tiles lie in one 128-row scale block, so every lane's own word serves all of them.
 //   MX:   lane l fetches the word of row l % 16 of tile (l / 16) % R.
 //   int4: lane l fetches the four rows 4 (l / 16) .. + 3 of tile (l % 16) % R.
@@ -65,7 +69,8 @@ struct Scales<MOE_W_INT4, G> {
 // A memory instruction costs its CU one cycle for every run of adjacent lanes that reads within 64 B.  In the MFMA
 // layout adjacent lanes hold different rows, which makes 64 such runs of 16 B; so the four lanes 4 r .. 4 r + 3 fetch
 // 64 B of row r, and the wavefront turns the 1 KiB piece into the MFMA layout through its own corner of LDS (LDS
-// instructions of one wavefront stay in order, so this takes no barrier).  The swizzle makes both the writes (eight
+// instructions of one wavefront stay in order, so this takes no barrier).  Before: the cache accesses were busy 85 % of
+// the time with 16 tokens (131072 x 7168 e2m1, 171 us; 115 since).  The swizzle makes both the writes (eight
 // lanes: two rows) and the reads (eight lanes: one 16 B column of eight rows) fall on distinct banks.
 constexpr int kCorner = 4 * 64;                              // 16 B elements of a wavefront's corner
 
@@ -328,18 +333,14 @@ __device__ __forceinline__ void block_product(Step<FMT, G, R, CT, XT>& st, uint3
         const u32x4 ones_bits = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
         uint32_t words[R];
         if constexpr (F::kMx) spread_rows<R>(st.s.w, words);
-        f32x4 sum[1] = {none};
-        if constexpr (F::kInt4) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                sum[0] = mfma(__builtin_bit_cast(bf16x8, ones_bits), token_values<XT>(st.x[0], q), sum[0]);
-            settle(sum);
-        }
+        f32x4 sum = none;                                    // int4: sum x, beside the first tiles
 #pragma unroll
         for (int r0 = 0; r0 < R; r0 += TG) {
-            f32x4 d[TG];
+            const bool sums = F::kInt4 && r0 == 0;
+            f32x4 d[F::kInt4 ? TG + 1 : TG];
 #pragma unroll
             for (int r = 0; r < TG; ++r) d[r] = F::kMx ? acc[r0 + r][0] : none;
+            if constexpr (F::kInt4) d[TG] = sum;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const bf16x8 b = token_values<XT>(st.x[0], q);
@@ -349,8 +350,11 @@ __device__ __forceinline__ void block_product(Step<FMT, G, R, CT, XT>& st, uint3
                     if constexpr (F::kMx) mx = e8m0_value(words[r0 + r], F::kFour ? g : 2 * (q >> 1) + (g >> 1));
                     d[r] = mfma(widen<FMT, G>(st.w[r0 + r], mx, q), b, d[r]);
                 }
+                if constexpr (F::kInt4)
+                    if (sums) d[TG] = mfma(__builtin_bit_cast(bf16x8, ones_bits), b, d[TG]);
             }
             settle(d);
+            if constexpr (F::kInt4) sum = d[TG];
 #pragma unroll
             for (int r = 0; r < TG; ++r) {
                 if constexpr (F::kMx) {
@@ -363,7 +367,7 @@ __device__ __forceinline__ void block_product(Step<FMT, G, R, CT, XT>& st, uint3
                         const uint32_t sw = tile_word<R>(st.s.s[i >> 1], r0 + r);
                         const float s = i & 1 ? bf16_hi(sw) : bf16_lo(sw);
                         const float z = (float)((zw >> (8 * i)) & 0xFFu);
-                        acc[r0 + r][0][i] = fmaf(s, fmaf(-z, sum[0][i], d[r][i]), acc[r0 + r][0][i]);
+                        acc[r0 + r][0][i] = fmaf(s, fmaf(-z, sum[i], d[r][i]), acc[r0 + r][0][i]);
                     }
                 } else {
                     const float s = __uint_as_float(st.s.w);

@@ -365,7 +365,8 @@ moe_status moe_combine(const moe_dims* dims, int32_t width, const uint16_t* y_bf
  * In:  logits float32 (logits_bf16 == 0) or bf16 bits (logits_bf16 != 0), row
  *      t at logits + t * logits_stride elements, logits_stride >= E.
  * Out: topk_ids int32 [T, k] (global expert ids);  topk_w float32 [T, k].
- * Uses T, k and E of dims.  E <= 1024 and k <= 64, else MOE_ERR_UNSUPPORTED.
+ * Uses T, k and E of dims.  E <= 1024, k <= 64 and T <= 2^25, else
+ * MOE_ERR_UNSUPPORTED.
  */
 moe_status moe_route_topk(const moe_dims* dims, const void* logits, int32_t logits_bf16,
                           int64_t logits_stride, int32_t renormalise, float scale,
@@ -409,8 +410,10 @@ typedef struct moe_weight {
 /*
  * Matrix-vector products: for row i < m and column c < n,
  *   y[i, c] = bf16( sum_j x[i, j] * w[c, j] )
- * in fp32 from the bf16 x and the exact weight values.  Made for a few rows
- * (the weights are read once per 64 rows); any m >= 0 is computed.
+ * in fp32 from the bf16 x and the exact weight values (e8m0 scales between
+ * 2^-100 and 2^100; MOE_W_INT4 takes x finite and below 2^100, and gives NaN
+ * for a row with an infinity).  Made for a few rows: the weights are read once
+ * per 64 rows.  m <= 2^20 and n <= 2^27, else MOE_ERR_UNSUPPORTED.
  * In:  x_bf16 bf16 bits, row i at x_bf16 + i * x_stride elements, 16-byte
  *      aligned, x_stride >= k and a multiple of 8 (below 2^24);
  *      w one matrix [n, k].
@@ -438,7 +441,10 @@ moe_status moe_few_token_layer_workspace(const moe_dims* dims, int32_t inter, si
  * Out: out_bf16 uint16 [T, H], 8-byte aligned.
  * ws: at least moe_few_token_layer_workspace bytes, 16-byte aligned, no
  * initialisation.  Tokens go through in batches of 64, each of which reads the
- * experts that it hits once; inter is a multiple of 128, L <= 1024, k <= 64.
+ * experts that it hits once (more often where an expert has far more tokens
+ * than uniform routing gives it); inter is a multiple of 128, L <= 1024,
+ * k <= 64.  No token's values enter another token's output; the order of a
+ * token's sums, and so its last rounding, may change with the batch.
  */
 moe_status moe_few_token_layer(const moe_dims* dims, int32_t inter, const uint16_t* x_bf16,
                                const int32_t* topk_ids, const float* topk_w, const moe_weight* w1,

@@ -114,6 +114,8 @@ def test_matvec_refusals(L):
         assert call(**bad) == -1, bad
     assert L.moe_matvec(2, 128, 256, FAKE, 256, None, FAKE, 128, None) == -1
     assert call(xs=1 << 24) == -3
+    assert call(m=(1 << 20) + 1) == -3
+    assert call(n=(1 << 27) + 4, ys=1 << 28) == -3
     assert L.moe_matvec(0, 128, 256, None, 256, _w(7), None, 128, None) == -1    # a bad weight, even with no rows
 
 
@@ -140,6 +142,7 @@ def test_layer_refusals(L):
     assert call(d=_dims(E=2048, L=2048)) == -3
     assert call(d=_dims(E=256, k=65)) == -3
     assert call(d=_dims(Ts=64, H=1 << 24)) == -3                  # 64 rows of 2^25 bytes
+    assert call(inter=1 << 24, nbytes=1 << 40) == -3
     assert call(d=_dims(Ts=64, k=64, E=64, L=64), inter=1 << 18, nbytes=1 << 40) == -3
     assert L.moe_few_token_layer(None, 128, *[FAKE] * 3, _w(), _w(), FAKE, FAKE, 1 << 20, None) == -1
     assert L.moe_few_token_layer(ctypes.byref(_dims().c()), 128, *[FAKE] * 3, None, _w(), FAKE, FAKE, 1 << 20, None) == -1
@@ -167,6 +170,7 @@ def test_route_topk_refusals(L):
         assert call(**bad) == -1, bad
     assert call(d=_dims(E=1025, L=8), stride=1025) == -3
     assert call(d=_dims(E=1024, k=65), stride=1024) == -3
+    assert call(d=_dims(Ts=(1 << 25) + 1)) == -3
 
 
 # ---------------------------------------------------------------- refusals of the binding
