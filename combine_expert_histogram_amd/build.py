@@ -12,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -59,10 +60,11 @@ def _link(sources: list[str], out: str, verbose: bool, extra: tuple[str, ...] = 
 
 
 def build(verbose: bool = False, trace: bool = True) -> str:
-    _link(CEILING_SOURCES, CEILING_LIB, verbose)
+    jobs = [(SOURCES, LIB, verbose), (CEILING_SOURCES, CEILING_LIB, verbose)]
     if trace:
-        _link(SOURCES, TRACE_LIB, verbose, ("-DMOE_TRACE=1",))
-    return _link(SOURCES, LIB, verbose)
+        jobs.append((SOURCES, TRACE_LIB, verbose, ("-DMOE_TRACE=1",)))
+    with ThreadPoolExecutor(len(jobs)) as pool:      # one hipcc each
+        return [f.result() for f in [pool.submit(_link, *job) for job in jobs]][0]
 
 
 if __name__ == "__main__":

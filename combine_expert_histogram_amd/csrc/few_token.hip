@@ -15,7 +15,11 @@ constexpr int kThreads = kWaves * MOE_WAVE;
 // K blocks a wavefront keeps in flight, and the wavefronts of a SIMD that its registers allow: two workgroups to a CU
 // hide each other's latencies (int4, groups of 128, 16 tokens: 99.7 -> 80.1 us for the gate and up products), which
 // one column tile allows unless an int4 format carries two or four scale groups a block (those would spill).
-constexpr int depth_of(int R, int CT, int XT) { return CT > 1 || R == 4 ? 1 : R == 2 || XT == 16 ? 2 : 4; }
+constexpr int depth_of(int FMT, int R, int CT, int XT) {
+    if (CT > 1) return 1;
+    if (R == 4) return FMT == MOE_W_E2M1_MX && XT < 16 ? 2 : 1;
+    return R == 2 || XT == 16 ? 2 : 4;
+}
 constexpr int waves_per_simd(int FMT, int G, int CT) { return CT == 1 && G == 1 ? 4 : 2; }
 constexpr int kChunk = 64;                 // tokens a layer launch handles: one lane each, four column tiles
 constexpr int kMaxTopK = 64;
@@ -40,7 +44,7 @@ __device__ __forceinline__ void store4(uint16_t* p, f32x4 v) {
 // follows each block.
 template <int FMT, int G, int R, int CT, int XT, class Load, class Done>
 __device__ __forceinline__ void stream_blocks(int n, Load&& load, u32x4* corner, f32x4 (&acc)[R][CT], Done&& done) {
-    constexpr int kDepth = depth_of(R, CT, XT);
+    constexpr int kDepth = depth_of(FMT, R, CT, XT);
     Step<FMT, G, R, CT, XT> st[kDepth];
     uint32_t cols[kDepth];
 #pragma unroll
@@ -133,13 +137,13 @@ matvec_wide_kernel(WView w, const uint16_t* __restrict__ x, int64_t ldx, int M, 
         [&](int t, int i) { return min(row0 + 16 * t + 4 * i, w.n - 4); });
     const __amdgpu_buffer_rsrc_t xb =
         row_buffer(x + col0 * ldx, (uint32_t)(((int64_t)(ncols - 1) * ldx + (int64_t)w.nb * kKBlock) * 2));
-    uint32_t at[kMine];                                      // piece p of token t: t * 16 + (p ^ t % 8)
+    uint32_t at[kMine];                                      // piece p of token t
     int to[kMine];
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
         const int id = threadIdx.x + kThreads * i, t = id >> 4, p = id & 15;
         at[i] = t < ncols ? (uint32_t)(t * ldx * 2 + 16 * p) : kNoRow;
-        to[i] = t * 16 + (p ^ (t & 7));
+        to[i] = t * 16 + (p ^ shared_swizzle<FMT>(t & 15));
     }
     u32x4 xr[kMine];
     const auto load_x = [&](int kb) {

@@ -9,8 +9,8 @@
 // 128 + q), so the products are those of the definition and the sums are fp32.  One token uses one column of the
 // sixteen: with 4-bit weights the matrix cores take 16 cycles of a CU for a KiB and column tile, the weight stream 90
 // (at 7 TB/s), so up to 64 tokens the stream is the floor.  What it comes to on one MI355X, us and TB/s of weights:
-//   131072 x 7168 e2m1: 1 token 92 (5.4), 16 tokens 115 (4.4), 64 tokens 140 (3.7)
-//   65536 x 7168 e4m3:  1 token 78 (6.0), 16 tokens 85 (5.6), 64 tokens 109 (4.4)
+//   131072 x 7168 e2m1: 1 token 91 (5.5), 16 tokens 115 (4.4), 64 tokens 136 (3.8)
+//   65536 x 7168 e4m3:  1 token 78 (6.0), 16 tokens 85 (5.6), 64 tokens 106 (4.5)
 //   131072 x 7168 int4, 1 token: groups of 128 98 (5.0), of 32 145 (3.9: vector instructions, 16 scales a row tile's
 //   block and lane to convert and apply)
 //
@@ -70,11 +70,12 @@ struct Scales<MOE_W_INT4, G> {
 // layout adjacent lanes hold different rows, which makes 64 such runs of 16 B; so the four lanes 4 r .. 4 r + 3 fetch
 // 64 B of row r, and the wavefront turns the 1 KiB piece into the MFMA layout through its own corner of LDS (LDS
 // instructions of one wavefront stay in order, so this takes no barrier).  Before: the cache accesses were busy 85 % of
-// the time with 16 tokens (131072 x 7168 e2m1, 171 us; 115 since).  The swizzle makes both the writes (eight
-// lanes: two rows) and the reads (eight lanes: one 16 B column of eight rows) fall on distinct banks.
+// the time with 16 tokens (131072 x 7168 e2m1, 171 us; 115 since).  The swizzle makes the eight
+// lanes that LDS serves at a time (four neighbours and four of the next sixteen lanes) fall on distinct banks, for the
+// writes (two rows) and the reads (one 16 B column of four rows, the next column of the other four).
 constexpr int kCorner = 4 * 64;                              // 16 B elements of a wavefront's corner
 
-__device__ __forceinline__ int turn_slot(int row, int piece) { return row * 4 + (piece ^ (row >> 1 & 3)); }
+__device__ __forceinline__ int turn_slot(int row, int piece) { return row * 4 + (piece ^ (row >> 1 & 3) ^ (row >> 3)); }
 
 __device__ __forceinline__ void turn_in(u32x4* lds, const u32x4& v) {
     const int l = lane_id();
@@ -466,8 +467,14 @@ __device__ __forceinline__ void settle_all(f32x4 (&d)[R][N]) {
     asm volatile("s_nop 15" : "+v"(d[0][0]));
 }
 
-// acc += one K block of weights in the MFMA layout times the tokens that the workgroup shares in LDS (piece p of token
-// t in element 16 t + (p ^ t % 8): eight lanes that read one piece of eight tokens meet eight distinct banks).
+// Tokens that a workgroup shares in LDS: piece p of token t in element 16 t + (p ^ shared_swizzle(t)).  LDS serves a
+// 16 B read eight lanes at a time, four of one sixteen with four of the next (lanes 0 to 3 with 20 to 23, and so on),
+// so the tokens t and t + 4 of neighbouring lane groups g, g + 1 have to differ in the low three bits: their pieces do
+// for e2m1 (4 g + q), the swizzle has to for the others.
+template <int FMT>
+__device__ __forceinline__ int shared_swizzle(int t) { return FMT == MOE_W_E2M1_MX ? t & 11 : t & 15; }
+
+// acc += one K block of weights in the MFMA layout times the tokens that the workgroup shares in LDS.
 template <int FMT, int G, int R, int CT>
 __device__ __forceinline__ void shared_product(const u32x4 (&w)[R][Fmt<FMT, G>::kLoads], const Scales<FMT, G>& s,
                                                const u32x4* xs, f32x4 (&acc)[R][CT]) {
@@ -476,7 +483,7 @@ __device__ __forceinline__ void shared_product(const u32x4 (&w)[R][Fmt<FMT, G>::
     const f32x4 none = {0.f, 0.f, 0.f, 0.f};
     const auto tokens = [&](int c, int q) {
         const int piece = x_offset<FMT, G>(q, g) / 8;
-        return __builtin_bit_cast(bf16x8, xs[(16 * c + c16) * 16 + (piece ^ (c16 & 7))]);
+        return __builtin_bit_cast(bf16x8, xs[(16 * c + c16) * 16 + (piece ^ shared_swizzle<FMT>(c16))]);
     };
     if constexpr (F::kInt4) {
         const u32x4 ones_bits = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
