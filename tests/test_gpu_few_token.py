@@ -164,6 +164,29 @@ def test_e8m0_range():
         check(got, xv @ exact.T, fp32_error(w, 0, xv, exact), f"{fmt} wide scales")
 
 
+def test_matvec_past_32_bits():
+    """A weight of more than 2^31 bytes and an output that starts past 2^31 elements: the last rows are what they are."""
+    require_gpu()
+    n, k, m = (1 << 17) + 128, 1 << 14, 2
+    rng = np.random.default_rng(0)
+    tail, exact = random_weight(rng, "e4m3_mx", 32, False, 128, k)
+    data = torch.zeros((n, k), dtype=torch.uint8, device="cuda")
+    data[-128:] = dev(tail["data"][0])
+    scale = torch.zeros((k // 128, n), dtype=torch.int32, device="cuda")
+    scale[:, -128:] = dev(tail["scale"][0].view(np.int32))
+    x = activations(rng, m, k)
+    got = moe.matvec(dev(x.view(np.int16)), moe.Weight("e4m3_mx", n, k, data, scale))
+    xv = values(x)
+    check(values(host_u16(got[:, -128:])), xv @ exact[0].T, fp32_error(tail, 0, xv, exact[0]), "far rows")
+    assert not got[:, :-128].any()
+    wide = torch.empty(((1 << 31) // 8192 + 8, 8192), dtype=torch.bfloat16, device="cuda")
+    view = wide[-4:, :128]
+    x4 = activations(rng, 4, 128)
+    w, exact = random_weight(rng, "e2m1_mx", 32, False, 128, 128)
+    moe.matvec(dev(x4.view(np.int16)), to_gpu(w), out=view)
+    check(values(host_u16(view)), values(x4) @ exact[0].T, fp32_error(w, 0, values(x4), exact[0]), "far output")
+
+
 # ---------------------------------------------------------------- the layer
 def make_layer(rng, T, E, e0, L, k, H, I, f1, f2=None):
     w1, x1 = random_weight(rng, *f1, 2 * I, H, L)
@@ -275,6 +298,25 @@ def test_layer_one_expert_in_every_slot(T, k):
     c["ids"][:] = 6
     c["tw"] /= k
     check_layer(c, run_layer(c), f"T={T} k={k}")
+
+
+def test_layer_of_a_far_expert():
+    """The last of 1024 experts, whose weights start past 2^31 bytes."""
+    require_gpu()
+    rng = np.random.default_rng(1)
+    L, H, I = 1024, 4224, 256
+    c = make_layer(rng, 3, L, L - 1, 1, 2, H, I, FORMATS[1])
+    c["ids"][:, 0] = L - 1
+    whole = []
+    for w in (c["w1"], c["w2"]):
+        data = torch.zeros((L, w["n"], w["k"]), dtype=torch.uint8, device="cuda")
+        scale = torch.zeros((L, w["k"] // 128, w["n"]), dtype=torch.int32, device="cuda")
+        data[-1], scale[-1] = dev(w["data"][0]), dev(w["scale"][0].view(np.int32))
+        whole.append(moe.Weight("e4m3_mx", w["n"], w["k"], data, scale, experts=L))
+    assert whole[0].data[:-1].numel() > 1 << 31
+    d = moe.Dims(S=1, Ts=3, k=2, E=L, e0=0, L=L, H=H)
+    got = moe.few_token_layer(d, I, dev(c["x"].view(np.int16)), dev(c["ids"]), dev(c["tw"]), *whole)
+    check_layer(c, got, "far expert")       # the other ids name experts of zeros
 
 
 def test_layer_nothing_local():
