@@ -557,7 +557,7 @@ constexpr int kCus = 256;
 
 // Row tiles of a wavefront of the wide product, and whether it pays: its workgroups take 256 rows each and want every
 // CU, while the plain form's token traffic grows with the column tiles.  us, plain form (four row tiles) / wide form:
-//   e2m1, K = 7168, 64 tokens: 16384 rows 29 / 68, 32768 rows 58 (twice that) / 70, 131072 rows 234 / 140
+//   e2m1, K = 7168, 64 tokens: 16384 rows 29 / 68, 32768 rows 58 (twice that) / 70, 131072 rows 234 / 136
 //   e2m1, K = 7168, 24 to 32 tokens: 16384 rows 21 / 58, 131072 rows 166 / 110;  e4m3, 64 tokens: 16384 rows 39 / 89
 // With four row tiles the wide form has half the LDS reads but one workgroup a CU, and takes the same (145 us).
 constexpr int kWideRows = 2;
@@ -617,7 +617,8 @@ extern "C" moe_status moe_few_token_layer_workspace(const moe_dims* dims, int32_
     moe_status st = load_dims(dims, &d, true);
     if (st != MOE_OK) return st;
     if (!bytes || inter < 128 || inter % 128 != 0) return MOE_ERR_INVALID_ARG;
-    if (d.L > kMaxLocal || d.k > kMaxTopK || inter >= (1 << 24)) return MOE_ERR_UNSUPPORTED;
+    // H and inter: the grids' limits
+    if (d.L > kMaxLocal || d.k > kMaxTopK || inter >= (1 << 24) || d.H >= (1 << 24)) return MOE_ERR_UNSUPPORTED;
     *bytes = (size_t)(std::min<int64_t>(d.T, kChunk) * d.k * inter * 2 + 255) / 256 * 256;
     return MOE_OK;
 }

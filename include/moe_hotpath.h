@@ -419,7 +419,7 @@ typedef struct moe_weight {
  *      w one matrix [n, k].
  * Out: y_bf16 bf16 bits, row i at y_bf16 + i * y_stride elements, 8-byte
  *      aligned, y_stride >= n and a multiple of 4.  Elements between the rows
- *      are not written.
+ *      are not written.  y overlaps neither x nor w.
  */
 moe_status moe_matvec(int32_t m, int32_t n, int32_t k, const uint16_t* x_bf16, int64_t x_stride,
                       const moe_weight* w, uint16_t* y_bf16, int64_t y_stride, void* hip_stream);
@@ -442,9 +442,12 @@ moe_status moe_few_token_layer_workspace(const moe_dims* dims, int32_t inter, si
  * ws: at least moe_few_token_layer_workspace bytes, 16-byte aligned, no
  * initialisation.  Tokens go through in batches of 64, each of which reads the
  * experts that it hits once (more often where an expert has far more tokens
- * than uniform routing gives it); inter is a multiple of 128, L <= 1024,
- * k <= 64.  No token's values enter another token's output; the order of a
- * token's sums, and so its last rounding, may change with the batch.
+ * than uniform routing gives it).  inter is a multiple of 128; H and inter
+ * below 2^24, min(T, 64) * H and min(T, 64) * k * inter below 2^30, L <= 1024
+ * and k <= 64, else MOE_ERR_UNSUPPORTED.  An int4 w1 takes x, and an int4 w2 the
+ * intermediate rows, in moe_matvec's range.  No output overlaps an input or ws.
+ * No token's values enter another token's output; the order of a token's sums,
+ * and so its last rounding, may change with the batch.
  */
 moe_status moe_few_token_layer(const moe_dims* dims, int32_t inter, const uint16_t* x_bf16,
                                const int32_t* topk_ids, const float* topk_w, const moe_weight* w1,

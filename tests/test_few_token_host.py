@@ -148,6 +148,15 @@ def test_layer_refusals(L):
     assert L.moe_few_token_layer(ctypes.byref(_dims().c()), 128, *[FAKE] * 3, None, _w(), FAKE, FAKE, 1 << 20, None) == -1
 
 
+def test_layer_widest_rows(L):
+    """hidden is refused from 2^24 on for one token too, by the workspace query as well."""
+    wide, need = _dims(Ts=1, H=1 << 24), ctypes.c_size_t()
+    args = (128, *[FAKE] * 3, _w(), _w(), FAKE, FAKE, 1 << 20, None)
+    assert L.moe_few_token_layer(ctypes.byref(wide.c()), *args) == -3
+    assert L.moe_few_token_layer_workspace(ctypes.byref(wide.c()), 128, ctypes.byref(need)) == -3
+    assert L.moe_few_token_layer_workspace(ctypes.byref(_dims(Ts=1, H=(1 << 24) - 128).c()), 128, ctypes.byref(need)) == 0
+
+
 def test_layer_workspace(L):
     assert b.moe_few_token_layer_workspace(_dims(), 128) == 4 * 2 * 128 * 2
     assert b.moe_few_token_layer_workspace(_dims(Ts=1, k=1), 128) == 256
