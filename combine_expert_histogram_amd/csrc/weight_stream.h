@@ -279,10 +279,10 @@ __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// Waits out the matrix pipeline before d is read.  An 8-pass MFMA's result may be read by the VALU 11 wait states
-// after it; the compiler counts them within straight code, but where it moved the reading instructions behind a
-// branch it left them out (seen in the listing: MFMA, s_cbranch, v_mov, v_fmac of the result, and a first component
-// short of the last two MFMAs).  The asm ties the wait to the values, so no branch can come between.
+// Waits out the matrix pipeline before d is read.  The result of this MFMA (four passes) may be read by the VALU eight
+// wait states after it, which is what the compiler leaves in straight code; where it moved the reading instructions
+// behind a branch it left them out (seen in the listing: MFMA, s_cbranch, v_mov, v_fmac of the result, and a first
+// component short of the last two MFMAs).  The asm ties the wait to the values, so no branch can come between.
 template <int N>
 __device__ __forceinline__ void settle(f32x4 (&d)[N]) {
     static_assert(N >= 1 && N <= 5, "tiles");
@@ -457,7 +457,8 @@ __device__ __forceinline__ void block_product(Step<FMT, G, R, CT, XT>& st, uint3
     }
 }
 
-// Ties the values of several tiles down before one wait for all of them.
+// The same for more tiles than one asm can name: all of them are tied down before the wait and again after it, so that
+// every read depends on an asm behind the wait (volatile ones keep their order; the empty ones emit nothing).
 template <int R, int N>
 __device__ __forceinline__ void settle_all(f32x4 (&d)[R][N]) {
 #pragma unroll
@@ -465,6 +466,10 @@ __device__ __forceinline__ void settle_all(f32x4 (&d)[R][N]) {
 #pragma unroll
         for (int c = 0; c < N; ++c) asm volatile("" : "+v"(d[r][c]));
     asm volatile("s_nop 15" : "+v"(d[0][0]));
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < N; ++c) asm volatile("" : "+v"(d[r][c]));
 }
 
 // Tokens that a workgroup shares in LDS: piece p of token t in element 16 t + (p ^ shared_swizzle(t)).  LDS serves a
