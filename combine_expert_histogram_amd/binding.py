@@ -469,9 +469,10 @@ class Weight:
 
 
 def _blocks_first(t: torch.Tensor, per_block: int) -> torch.Tensor:
-    """[.., n, k/128 * per_block] -> contiguous [.., k/128, n, per_block]"""
+    """[.., n, k/128 * per_block] -> contiguous [.., k/128, n, per_block], always a copy (with one K block the transposed
+    view is contiguous already)"""
     t = t.unflatten(-1, (-1, per_block))
-    return t.transpose(-3, -2).contiguous()
+    return t.transpose(-3, -2).clone(memory_format=torch.contiguous_format)
 
 
 def _pack_nibbles(q: torch.Tensor) -> torch.Tensor:
