@@ -491,8 +491,8 @@ def int4_weight(q: torch.Tensor, scale: torch.Tensor, zero: torch.Tensor | None 
     group = k // max(scale.shape[-1], 1)
     if group not in (32, 64, 128) or scale.shape[-1] * group != k:
         raise ValueError("scale must have k/32, k/64 or k/128 columns")
-    if int(q.max()) > 15 or (zero is not None and not 0 <= int(zero.min()) <= int(zero.max()) <= 15):
-        raise ValueError("codes and zero points must be in 0..15")
+    if int(q.max()) > 15 or (zero is not None and not bool(((zero >= 0) & (zero <= 15) & (zero % 1 == 0)).all())):
+        raise ValueError("codes and zero points must be whole numbers in 0..15")
     # k = 32 s + 8 g + 2 h + b of a block is nibble 4 b + h of word 4 g + s
     w = q.unflatten(-1, (k // 128, 4, 4, 4, 2))
     lead = w.dim() - 4

@@ -49,3 +49,14 @@ def test_e2m1_packer_takes_any_view_and_keeps_its_own_copy(k):
     for t in views:
         t.zero_()
     np.testing.assert_array_equal(values(), want)
+
+
+def test_int4_packer_refuses_zero_points_that_are_not_whole():
+    q, s = torch.zeros((8, 128), dtype=torch.uint8), torch.ones((8, 4))
+    whole = torch.full((8, 4), 7.0)
+    assert (moe.int4_weight(q, s, whole).zero == 7).all()
+    for value in (7.5, 0.25, float("nan"), float("inf")):
+        bad = whole.clone()
+        bad[3, 1] = value
+        with pytest.raises(ValueError):
+            moe.int4_weight(q, s, bad)
