@@ -418,6 +418,7 @@ def combine(d: Dims, width: int, y_bf16, assign_row, topk_w, out=None):
 WEIGHT_FORMATS = {"e4m3": 0, "e4m3_mx": 1, "e2m1_mx": 2, "int4": 3}
 _BF16_BITS = (torch.bfloat16, torch.int16, torch.uint16)
 _PACKED = (torch.int32, torch.uint32)
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
 
 
 class Weight:
@@ -436,7 +437,10 @@ class Weight:
         if fmt != "int4" and zero is not None:
             raise ValueError("zero points belong to int4 weights")
         numel, blocks = experts * n * k, experts * n * (k // 128)
-        self._tensor(data, "data", (torch.uint8,), numel // (2 if fmt in ("e2m1_mx", "int4") else 1))
+        if fmt in ("e2m1_mx", "int4"):
+            self._tensor(data, "data", (torch.uint8,), numel // 2)
+        else:
+            self._tensor(data, "data", _E4M3, numel)
         if fmt == "e4m3":
             self._tensor(scale, "scale", (torch.float32,), blocks // 128)
         elif fmt == "int4":
