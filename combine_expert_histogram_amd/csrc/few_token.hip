@@ -565,11 +565,16 @@ constexpr int64_t kWideGroupRows = kWaves * 16 * kWideRows;
 bool wide_pays(int64_t n, int64_t m) { return m > 16 && n >= kCus * kWideGroupRows; }
 
 // Row tiles of a wavefront: the more, the fewer token loads a weight load takes beside it, as long as there is a
-// workgroup for every CU.  us with 1 / 2 / 4 of them (e2m1): 4096 x 7168, 1 token: 6.2 / 7.5 / 11.6; 16384 x 4096, 16
-// tokens: - / 12.5 / 11.2; 131072 x 7168, 16 tokens: - / 140 / 115.
-int matvec_rows(int64_t n) {
+// workgroup for every CU.  us with 1 / 2 / 4 of them: 4096 x 7168 e2m1, 1 token: 6.2 / 7.5 / 11.6; 16384 x 4096 e2m1, 16
+// tokens: - / 12.5 / 11.2; 131072 x 7168 e2m1, 16 tokens: - / 140 / 115; 16384 x 7168, 24 tokens: e2m1 33 / 24 / 21,
+// e4m3 39 / 30 / 26, int4 in groups of 128 35 / 28 / 23, of 32 41 / 40 / 35; 64 tokens: e2m1 55 / 39 / 29, e4m3 66 / 46 /
+// 39.  int4 takes two at most beside four column tiles: four would keep 59 to 95 registers of a lane in scratch memory
+// (16384 x 7168, 64 tokens, groups of 128 / 64 / 32: one 65 / 73 / 92, two 42 / 48 / 63, four 79 / 75 / 110).
+constexpr int most_rows(int FMT, int CT) { return FMT == MOE_W_INT4 && CT == 4 ? 2 : 4; }
+
+int matvec_rows(int64_t n, int most) {
     int r = 1;
-    while (r < 4 && n >= 16 * 2 * r * kCus) r *= 2;
+    while (r < most && n >= 16 * 2 * r * kCus) r *= 2;
     return r;
 }
 
@@ -606,7 +611,9 @@ extern "C" moe_status moe_matvec(int32_t m, int32_t n, int32_t k, const uint16_t
                 matvec_kernel<fmt, g, r, ct, xt><<<grid, kThreads, 0, stream>>>(v, x_bf16, x_stride, m, y_bf16,
                                                                                y_stride);
             };
-            with_rows<1, 2, 4>(matvec_rows(n), launch);
+            constexpr int most = most_rows(fmt, ct);
+            if constexpr (most == 4) with_rows<1, 2, 4>(matvec_rows(n, most), launch);
+            else with_rows<1, 2>(matvec_rows(n, most), launch);
         });
         return launch_status();
     });
