@@ -14,7 +14,10 @@ constexpr int kWaves = 8;                  // wavefronts of a workgroup; they sp
 constexpr int kThreads = kWaves * MOE_WAVE;
 // K blocks a wavefront keeps in flight, and the wavefronts of a SIMD that its registers allow: two workgroups to a CU
 // hide each other's latencies (int4, groups of 128, 16 tokens: 99.7 -> 80.1 us for the gate and up products), which
-// one column tile allows unless an int4 format carries two or four scale groups a block (those would spill).
+// one column tile allows unless an int4 format carries two or four scale groups a block: under that limit their loops
+// would keep up to 52 and 158 registers of a lane in scratch memory.  A few kernels keep some there within the limits
+// taken: matvec e4m3 with four row and four column tiles 6 (16384 x 7168, 64 tokens: 39 us, against 46 with two row
+// tiles and none), gate_up int4 in groups of 32 with four row tiles 2, and the down kernels named at down_waves.
 constexpr int depth_of(int FMT, int R, int CT, int XT) {
     if (CT > 1) return 1;
     if (R == 4) return FMT == MOE_W_E2M1_MX && XT < 16 ? 2 : 1;
@@ -121,9 +124,10 @@ matvec_kernel(WView w, const uint16_t* __restrict__ x, int64_t ldx, int M, uint1
 // More than sixteen tokens against many rows: here the tokens' values are the larger stream (sixteen rows of 64 tokens
 // read 16 KiB of them beside 1 or 2 KiB of weights), so the eight wavefronts share them.  Each takes 16 R rows over the
 // whole of K; a block's token values go through LDS once (two buffers, one barrier a block), and the weights of two
-// blocks are in flight in registers.  64 tokens, 131072 x 7168 e2m1: 136 us, 0.88 PFLOP/s, bound by the matrix cores at
-// the clock their power leaves (2.0 to 2.1 GHz, 0.40 busy; a large library product reaches 1.26 PFLOP/s); 65536 x 7168
-// e4m3 106 us, 4.5 TB/s.
+// blocks are in flight in registers.  64 tokens, 131072 x 7168 e2m1: 136 to 146 us, 0.85 PFLOP/s (a large library
+// product reaches 1.26), at 2.0 to 2.1 GHz.  No unit is the limit by itself (matrix cores 0.40 busy, LDS 0.35, loads
+// 0.54): a block's turn, token reads and products follow each other, with a barrier for the workgroup.  65536 x 7168 e4m3
+// 106 to 110 us, 4.4 TB/s; 131072 x 7168 int4 206 to 214 (groups of 128), 316 (of 32).
 template <int FMT, int G, int R, int CT>
 __global__ void __launch_bounds__(kThreads)
 matvec_wide_kernel(WView w, const uint16_t* __restrict__ x, int64_t ldx, int M, uint16_t* __restrict__ y, int64_t ldy) {
@@ -270,9 +274,11 @@ __device__ __forceinline__ uint64_t tokens_of(const LayerArgs& a, const int32_t*
 // First launch: h[t k + j] = w (silu(gate) up) in bf16, for the first slot j in which token t names the expert, w
 // the sum of the token's weights for it.  A workgroup takes 8 R columns of h of one expert: a tile's sixteen weight
 // rows are eight gate rows and the eight up rows that go with them.  The rounding of h to bf16 is the matrix
-// instruction's input type; it is of the size of the output's own.
+// instruction's input type; it is of the size of the output's own (a layer is off by 2.35e-3 of its size against 64
+// bits, by 1.66e-3 with h in fp32).  The hardware exponential is off by a few 2^-24 and |gate| 2^-24, far below that.
 // One token, 8 experts of 2 x 2048 x 7168 e2m1: 27.8 us, 4.5 TB/s, of which the start (launch, ids, lists, first round
-// trip) is about 8; 64 tokens, 28 experts e4m3: 120 to 138 us, 6 TB/s.
+// trip) is about 8; 64 tokens, 28 experts e4m3: 120 to 138 us, 6 TB/s.  An expert that every token names takes its passes
+// one after the other in its own workgroups (that layer with one such expert: 209 -> 244 us; int4 of 128 152 -> 198).
 template <int FMT, int G, int R, int CT, int XT>
 __global__ void __launch_bounds__(kThreads, waves_per_simd(FMT, G, CT))
 gate_up_kernel(WView w, LayerArgs a) {
@@ -399,7 +405,11 @@ __device__ __forceinline__ int list_passes(const LayerArgs& a, const int32_t* id
 
 // Wavefronts of a down workgroup.  One row tile is taken where the rows give every CU only one workgroup, which then
 // needs sixteen to hide a block's latency (4096 rows, int4, 16 tokens: 52.4 us with eight, 42.4 with sixteen; with two
-// row tiles both take the same); more scale groups would spill and four output tiles would not fit LDS.
+// row tiles both take the same); more scale groups would spill (up to 39 and 147 registers a lane) and four output tiles
+// would not fit LDS.  Three of the kernels at 128 registers keep 2 to 7 in scratch memory.  Those with two row tiles and
+// sixteen tokens' columns would be a little faster at two wavefronts a SIMD without (the layer, 16 tokens, 4 of 8
+// experts, H = 7168: e4m3 71.2 against 69.5 us, int4 58.4 against 55.8); int4 with one row tile and eight takes the same
+// either way (24 tokens, H = 4096: 65.3, with eight wavefronts 65.4).
 constexpr int down_waves(int G, int R, int OT) { return R == 1 && OT <= 2 && G == 1 ? 16 : 8; }
 
 // Second launch: out[t] = sum over the experts of W2[e] h[t, e], one long product whose K runs over the experts hit
@@ -556,10 +566,19 @@ void with_rows(int r, F&& f) {
 constexpr int kCus = 256;
 
 // Row tiles of a wavefront of the wide product, and whether it pays: its workgroups take 256 rows each and want every
-// CU, while the plain form's token traffic grows with the column tiles.  us, plain form (four row tiles) / wide form:
-//   e2m1, K = 7168, 64 tokens: 16384 rows 29 / 68, 32768 rows 58 (twice that) / 70, 131072 rows 234 / 136
-//   e2m1, K = 7168, 24 to 32 tokens: 16384 rows 21 / 58, 131072 rows 166 / 110;  e4m3, 64 tokens: 16384 rows 39 / 89
-// With four row tiles the wide form has half the LDS reads but one workgroup a CU, and takes the same (145 us).
+// CU, while the plain form's token traffic grows with the column tiles.  us at K = 7168, plain form / wide form:
+//                          16384 rows   32768 rows   65536 rows   131072 rows
+//   e2m1, 24 tokens           21 / 58      39 / 60      73 / 66     142 / 108
+//   e2m1, 64 tokens           29 / 67      53 / 69     101 / 79     196 / 142
+//   e4m3, 24 tokens           26 / 74      49 / 77      94 / 95     187 / 164
+//   e4m3, 64 tokens           39 / 90      73 / 92     143 / 110    282 / 216     (e4m3_mx: the same within 7 %)
+//   int4 of 128, 24 tokens    23 / 76      42 / 76      80 / 80     156 / 135
+//   int4 of 128, 64 tokens    43 / 100     82 / 100    158 / 107    311 / 214
+//   int4 of 32, 24 tokens     33 / 116     63 / 117    122 / 119    239 / 235
+//   int4 of 32, 64 tokens     63 / 155    122 / 157    240 / 159    475 / 316
+// With four row tiles the wide form has half the LDS reads but one workgroup a CU, and takes the same (e2m1, 64 tokens,
+// 131072 rows: 145 us).  Both forms step up where a workgroup more no longer fits the CUs at once (17 tokens, int4 of
+// 32: 16384 rows 33 us, 16388 rows 55).
 constexpr int kWideRows = 2;
 constexpr int64_t kWideGroupRows = kWaves * 16 * kWideRows;
 bool wide_pays(int64_t n, int64_t m) { return m > 16 && n >= kCus * kWideGroupRows; }
@@ -683,8 +702,10 @@ extern "C" moe_status moe_few_token_layer(const moe_dims* dims, int32_t inter, c
             return launch_status();
         });
         if (st != MOE_OK) return st;
-        // two row tiles from three quarters of a workgroup a CU: 7168 rows 17.3 us against 22.4 with one (one token,
-        // e2m1); 4096 rows 67 against 57 (16 tokens, int4)
+        // two row tiles from three quarters of a workgroup a CU.  The layer's us with one / two (I = 2048; one token and
+        // 8 experts e2m1, 16 tokens and 21 experts int4, 64 tokens and 28 experts e4m3): 4096 rows 29 / 31, 59 / 70,
+        // 127 / 140; 5120 rows 41 / 37, 83 / 77, 176 / 162 (a second round of workgroups: two would pay here already);
+        // 6144 rows 44 / 40, 92 / 85, 198 / 186; 7168 rows 49 / 45, 98 / 92, 216 / 210
         const int r2 = d.H >= 24 * kCus ? 2 : 1;
         st = with_format(w2->format, g2, [&](auto fmt, auto g) {
             with_cols(std::min<int64_t>(share, 16), [&](auto ct, auto xt) {

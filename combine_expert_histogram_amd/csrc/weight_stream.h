@@ -9,10 +9,15 @@
 // 128 + q), so the products are those of the definition and the sums are fp32.  One token uses one column of the
 // sixteen: with 4-bit weights the matrix cores take 16 cycles of a CU for a KiB and column tile, the weight stream 90
 // (at 7 TB/s), so up to 64 tokens the stream is the floor.  What it comes to on one MI355X, us and TB/s of weights:
-//   131072 x 7168 e2m1: 1 token 91 (5.5), 16 tokens 115 (4.4), 64 tokens 136 (3.8)
-//   65536 x 7168 e4m3:  1 token 78 (6.0), 16 tokens 85 (5.6), 64 tokens 106 (4.5)
+//   131072 x 7168 e2m1: 1 token 91 (5.5), 16 tokens 115 (4.4), 64 tokens 136 to 146 (3.7)
+//   65536 x 7168 e4m3:  1 token 78 (6.0), 16 tokens 85 (5.6), 64 tokens 106 to 110 (4.4); e4m3_mx 81, 86, 109
 //   131072 x 7168 int4, 1 token: groups of 128 98 (5.0), of 32 145 (3.9: vector instructions, 16 scales a row tile's
-//   block and lane to convert and apply)
+//   block and lane to convert and apply); 16 tokens 119 and 154
+//
+// An integer is widened as 128 + q, and a group's sum corrected by (128 + zero) times the sum of x.  The two sums are up
+// to 143 scales of sum |x| where (q - zero) x itself stays below 15, so three to four of fp32's bits go to the
+// difference: an error of about 1e-5 of an ordinary group's sum, unseen in a bf16 output unless the groups cancel.
+// Exact signed values would take a conversion an element where this takes a mask and an or for two.
 //
 // Which k a lane holds is free as long as both operands agree.  A lane always loads 16 B of one weight row, four
 // lanes cover 64 B of it, and the K order of the MFMAs follows from that:

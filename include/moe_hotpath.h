@@ -412,9 +412,10 @@ typedef struct moe_weight {
  *   y[i, c] = bf16( sum_j x[i, j] * w[c, j] )
  * in fp32 from the bf16 x and the exact weight values (e8m0 scales between
  * 2^-100 and 2^100, and any code but 255 for a group of zeros; MOE_W_INT4 takes
- * x finite and below 2^100, and gives NaN for a row with an infinity).  Made
- * for a few rows: the weights are read once per 64 rows.  m <= 2^20 and
- * n <= 2^27, else MOE_ERR_UNSUPPORTED.
+ * x finite and below 2^100, gives NaN for a row with an infinity, and sums
+ * (128 + q) x and (128 + zero) x apart, so that its fp32 roundings are relative
+ * to up to 143 scales of sum |x|).  Made for a few rows: the weights are read
+ * once per 64 rows.  m <= 2^20 and n <= 2^27, else MOE_ERR_UNSUPPORTED.
  * In:  x_bf16 bf16 bits, row i at x_bf16 + i * x_stride elements, 16-byte
  *      aligned, x_stride >= k and a multiple of 8 (below 2^24);
  *      w one matrix [n, k].
