@@ -27,7 +27,10 @@ EXPORTS = ("moe_status_string", "moe_capacity", "moe_route_layout_workspace", "m
            "moe_quant_dispatch_mx", "moe_grouped_gemm1_mx", "moe_silu_mul_quant",
            "moe_grouped_gemm2_workspace", "moe_grouped_gemm2", "moe_silu_mul_quant_mx",
            "moe_grouped_gemm2_mx", "moe_combine", "moe_route_topk", "moe_matvec",
-           "moe_few_token_layer_workspace", "moe_few_token_layer")
+           "moe_few_token_layer_workspace", "moe_few_token_layer", "moe_layer_norm",
+           "moe_layer_norm_backward_workspace", "moe_layer_norm_backward", "moe_linear_workspace", "moe_linear",
+           "moe_linear_backward_workspace", "moe_linear_backward", "moe_gated_linear_workspace", "moe_gated_linear",
+           "moe_gated_linear_backward_workspace", "moe_gated_linear_backward")
 
 
 class MoeError(RuntimeError):
@@ -101,6 +104,17 @@ def lib() -> ctypes.CDLL:
             "moe_few_token_layer_workspace": (I32, [D, I32, ctypes.POINTER(SZ)]),
             "moe_few_token_layer": (I32, [D, I32, P, P, P, ctypes.POINTER(moe_weight),
                                           ctypes.POINTER(moe_weight), P, P, SZ, P]),
+            "moe_layer_norm": (I32, [I32] * 4 + [P, I64, P, P, ctypes.c_float, P, I64, P, P, P]),
+            "moe_layer_norm_backward_workspace": (I32, [I32, I32, ctypes.POINTER(SZ)]),
+            "moe_layer_norm_backward": (I32, [I32] * 4 + [P, I64, P, I64, P, P, P, P, I64, P, P, P, SZ, P]),
+            "moe_linear_workspace": (I32, [I32] * 3 + [ctypes.POINTER(SZ)]),
+            "moe_linear": (I32, [I32] * 4 + [P, I64, P, I64, P, I32, P, I64, P, I64, P, I64, P, SZ, P]),
+            "moe_linear_backward_workspace": (I32, [I32] * 4 + [ctypes.POINTER(SZ)]),
+            "moe_linear_backward": (I32, [I32] * 4 + [P, I64] * 3 + [I32] + [P, I64] * 3 + [P, P, SZ, P]),
+            "moe_gated_linear_workspace": (I32, [I32] * 3 + [ctypes.POINTER(SZ)]),
+            "moe_gated_linear": (I32, [I32] * 4 + [P, I64] * 2 + [I32] + [P, I64] * 2 + [P, SZ, P]),
+            "moe_gated_linear_backward_workspace": (I32, [I32] * 3 + [ctypes.POINTER(SZ)]),
+            "moe_gated_linear_backward": (I32, [I32] * 4 + [P, I64] * 4 + [I32] + [P, I64] * 2 + [P, SZ, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -627,3 +641,262 @@ def few_token_layer(d: Dims, inter: int, x, topk_ids, topk_w, w1: Weight, w2: We
     ws = alloc_few_token_workspace(d, inter, x.device) if ws is None else ws
     moe_few_token_layer(d, inter, x, topk_ids, topk_w, w1, w2, out, ws)
     return out
+
+
+# ---------------------------------------------------------------- the dense half, forward and backward
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def _act(act: str) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
+    return ACTIVATIONS[act]
+
+
+def _matrix(t, name: str, rows: int, cols: int, like) -> tuple[int | None, int]:
+    """(pointer, row stride) of an optional [rows, cols] matrix of `like`'s type and device."""
+    if t is None:
+        return None, cols
+    if t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
+    return t.data_ptr(), _rows(t, name, rows, cols)
+
+
+def _vector(t, name: str, n: int, dtype, device) -> int | None:
+    """Pointer of an optional contiguous [n] vector."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.device != device or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{n}] vector of {dtype} on {device}, got {tuple(t.shape)} of "
+                         f"{t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def _two_dims(t, name: str, dtypes) -> tuple[int, int]:
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a device tensor")
+    _dtype(t, name, dtypes)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got {tuple(t.shape)}")
+    return t.shape
+
+
+def _workspace(ws, device) -> tuple[int | None, int]:
+    if ws is None:
+        return None, 0
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous and on {device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+_HALF = (torch.bfloat16, torch.float16)
+
+
+def _bytes(fn: str, *args: int) -> int:
+    b = ctypes.c_size_t()
+    _check(fn, getattr(_lib or lib(), fn)(*args, ctypes.byref(b)))
+    return b.value
+
+
+def moe_layer_norm_backward_workspace(rows: int, cols: int) -> int:
+    return _bytes("moe_layer_norm_backward_workspace", rows, cols)
+
+
+def moe_linear_workspace(m: int, n: int, k: int) -> int:
+    return _bytes("moe_linear_workspace", m, n, k)
+
+
+def moe_linear_backward_workspace(m: int, n: int, k: int, act: str) -> int:
+    return _bytes("moe_linear_backward_workspace", m, n, k, _act(act))
+
+
+def moe_gated_linear_workspace(m: int, inter: int, hidden: int) -> int:
+    return _bytes("moe_gated_linear_workspace", m, inter, hidden)
+
+
+def moe_gated_linear_backward_workspace(m: int, inter: int, hidden: int) -> int:
+    return _bytes("moe_gated_linear_backward_workspace", m, inter, hidden)
+
+
+def _param_dtype(x, weight, bias):
+    p = next((t.dtype for t in (weight, bias) if t is not None), x.dtype)
+    if p not in (x.dtype, torch.float32):
+        raise ValueError(f"parameters must be {x.dtype} or float32, got {p}")
+    return p
+
+
+def moe_layer_norm(x, weight, bias, eps: float, y, mean, rstd) -> None:
+    rows, cols = _two_dims(x, "x", tuple(DTYPES))
+    p, dev = _param_dtype(x, weight, bias), x.device
+    xs = _rows(x, "x", rows, cols)
+    yp, ys = _matrix(y, "y", rows, cols, x)
+    _launch(dev, "moe_layer_norm", rows, cols, DTYPES[x.dtype], DTYPES[p], x.data_ptr(), xs,
+            _vector(weight, "weight", cols, p, dev), _vector(bias, "bias", cols, p, dev), float(eps), yp, ys,
+            _vector(mean, "mean", rows, torch.float32, dev), _vector(rstd, "rstd", rows, torch.float32, dev))
+
+
+def moe_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws) -> None:
+    rows, cols = _two_dims(x, "x", tuple(DTYPES))
+    p, dev = _param_dtype(x, weight if weight is not None else dweight, dbias), x.device
+    xs = _rows(x, "x", rows, cols)
+    dyp, dys = _matrix(dy, "dy", rows, cols, x)
+    dxp, dxs = _matrix(dx, "dx", rows, cols, x)
+    wp, wb = _workspace(ws, dev)
+    _launch(dev, "moe_layer_norm_backward", rows, cols, DTYPES[x.dtype], DTYPES[p], dyp, dys, x.data_ptr(), xs,
+            _vector(weight, "weight", cols, p, dev), _vector(mean, "mean", rows, torch.float32, dev),
+            _vector(rstd, "rstd", rows, torch.float32, dev), dxp, dxs, _vector(dweight, "dweight", cols, p, dev),
+            _vector(dbias, "dbias", cols, p, dev), wp, wb)
+
+
+def moe_linear(x, w, bias, act: str, residual, z, y, ws) -> None:
+    m, k = _two_dims(x, "x", _HALF)
+    n = _two_dims(w, "w", _HALF)[0]
+    xs = _rows(x, "x", m, k)
+    wp, wst = _matrix(w, "w", n, k, x)
+    rp, rs = _matrix(residual, "residual", m, n, x)
+    zp, zs = _matrix(z, "z", m, n, x)
+    yp, ys = _matrix(y, "y", m, n, x)
+    sp, sb = _workspace(ws, x.device)
+    _launch(x.device, "moe_linear", m, n, k, DTYPES[x.dtype], x.data_ptr(), xs, wp, wst,
+            _vector(bias, "bias", n, x.dtype, x.device), _act(act), rp, rs, zp, zs, yp, ys, sp, sb)
+
+
+def moe_linear_backward(dy, x, w, act: str, z, dx, dw, dbias, ws) -> None:
+    """x may be None without dw, w without dx; then their sizes are the outputs'."""
+    m, n = _two_dims(dy, "dy", _HALF)
+    of = next((t for t in (x, w, dx, dw) if t is not None), None)
+    k = 1 if of is None else _two_dims(of, "x, w, dx or dw", _HALF)[1]
+    dys = _rows(dy, "dy", m, n)
+    xp, xs = _matrix(x, "x", m, k, dy)
+    wp, wst = _matrix(w, "w", n, k, dy)
+    zp, zs = _matrix(z, "z", m, n, dy)
+    dxp, dxs = _matrix(dx, "dx", m, k, dy)
+    dwp, dws = _matrix(dw, "dw", n, k, dy)
+    sp, sb = _workspace(ws, dy.device)
+    _launch(dy.device, "moe_linear_backward", m, n, k, DTYPES[dy.dtype], dy.data_ptr(), dys, xp, xs, wp, wst, _act(act),
+            zp, zs, dxp, dxs, dwp, dws, _vector(dbias, "dbias", n, dy.dtype, dy.device), sp, sb)
+
+
+def _inter(w) -> int:
+    n = _two_dims(w, "w", _HALF)[0]
+    if n < 2 or n % 2:
+        raise ValueError(f"w must hold the gate's rows and as many of the up projection's, got {n}")
+    return n // 2
+
+
+def moe_gated_linear(x, w, act: str, gu, h, ws) -> None:
+    m, k = _two_dims(x, "x", _HALF)
+    inter = _inter(w)
+    xs = _rows(x, "x", m, k)
+    wp, wst = _matrix(w, "w", 2 * inter, k, x)
+    gp, gs = _matrix(gu, "gu", m, 2 * inter, x)
+    hp, hs = _matrix(h, "h", m, inter, x)
+    sp, sb = _workspace(ws, x.device)
+    _launch(x.device, "moe_gated_linear", m, inter, k, DTYPES[x.dtype], x.data_ptr(), xs, wp, wst, _act(act), gp, gs, hp,
+            hs, sp, sb)
+
+
+def moe_gated_linear_backward(dh, x, w, gu, act: str, dx, dw, ws) -> None:
+    """x may be None without dw, w without dx."""
+    m, inter = _two_dims(dh, "dh", _HALF)
+    of = next((t for t in (x, w, dx, dw) if t is not None), None)
+    k = 1 if of is None else _two_dims(of, "x, w, dx or dw", _HALF)[1]
+    dhs = _rows(dh, "dh", m, inter)
+    gp, gs = _matrix(gu, "gu", m, 2 * inter, dh)
+    xp, xs = _matrix(x, "x", m, k, dh)
+    wp, wst = _matrix(w, "w", 2 * inter, k, dh)
+    dxp, dxs = _matrix(dx, "dx", m, k, dh)
+    dwp, dws = _matrix(dw, "dw", 2 * inter, k, dh)
+    sp, sb = _workspace(ws, dh.device)
+    _launch(dh.device, "moe_gated_linear_backward", m, inter, k, DTYPES[dh.dtype], dh.data_ptr(), dhs, gp, gs, xp, xs, wp,
+            wst, _act(act), dxp, dxs, dwp, dws, sp, sb)
+
+
+def _alloc_bytes(n: int, device) -> torch.Tensor:
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def alloc_layer_norm_backward_workspace(rows: int, cols: int, device="cuda") -> torch.Tensor:
+    return _alloc_bytes(moe_layer_norm_backward_workspace(rows, cols), device)
+
+
+def alloc_linear_workspace(m: int, n: int, k: int, device="cuda") -> torch.Tensor:
+    return _alloc_bytes(moe_linear_workspace(m, n, k), device)
+
+
+def alloc_linear_backward_workspace(m: int, n: int, k: int, act: str = "none", device="cuda") -> torch.Tensor:
+    return _alloc_bytes(moe_linear_backward_workspace(m, n, k, act), device)
+
+
+def alloc_gated_linear_workspace(m: int, inter: int, hidden: int, device="cuda") -> torch.Tensor:
+    return _alloc_bytes(moe_gated_linear_workspace(m, inter, hidden), device)
+
+
+def alloc_gated_linear_backward_workspace(m: int, inter: int, hidden: int, device="cuda") -> torch.Tensor:
+    return _alloc_bytes(moe_gated_linear_backward_workspace(m, inter, hidden), device)
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, mean=None, rstd=None):
+    """x [rows, cols] (bfloat16, float16 or float32), weight and bias [cols] of x's type or float32 -> [rows, cols].  mean
+    and rstd, float32 [rows], are filled in where given: layer_norm_backward reads them."""
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    moe_layer_norm(x, weight, bias, eps, out, mean, rstd)
+    return out
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, bias: bool = True, dx=None, dweight=None, dbias=None, ws=None):
+    """(dx, dweight, dbias) of layer_norm; dweight is None without a weight, dbias without `bias`."""
+    rows, cols = x.shape
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx is None else dx
+    if weight is not None and dweight is None:
+        dweight = torch.empty_like(weight)
+    if bias and dbias is None:
+        dbias = torch.empty(cols, dtype=x.dtype if weight is None else weight.dtype, device=x.device)
+    ws = alloc_layer_norm_backward_workspace(rows, cols, x.device) if ws is None else ws
+    moe_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws)
+    return dx, dweight, dbias
+
+
+def linear(x, w, bias=None, act: str = "none", residual=None, z=None, out=None, ws=None):
+    """act(x w^T + bias) + residual: x [m, k], w [n, k] (bfloat16 or float16) -> [m, n].  z [m, n] is filled with
+    x w^T + bias where given: linear_backward reads it."""
+    m, k, n = x.shape[0], x.shape[-1], w.shape[0]
+    out = torch.empty((m, n), dtype=x.dtype, device=x.device) if out is None else out
+    if ws is None and moe_linear_workspace(m, n, k):
+        ws = alloc_linear_workspace(m, n, k, x.device)
+    moe_linear(x, w, bias, act, residual, z, out, ws)
+    return out
+
+
+def linear_backward(dy, x, w, act: str = "none", z=None, bias: bool = True, dx=None, dw=None, dbias=None, ws=None):
+    """(dx, dw, dbias) of linear; dbias is None without `bias`.  z as linear left it (not needed without an activation)."""
+    (m, n), k = dy.shape, x.shape[-1]
+    dx = torch.empty((m, k), dtype=dy.dtype, device=dy.device) if dx is None else dx
+    dw = torch.empty((n, k), dtype=dy.dtype, device=dy.device) if dw is None else dw
+    if bias and dbias is None:
+        dbias = torch.empty(n, dtype=dy.dtype, device=dy.device)
+    ws = alloc_linear_backward_workspace(m, n, k, act, dy.device) if ws is None else ws
+    moe_linear_backward(dy, x, w, act, z, dx, dw, dbias, ws)
+    return dx, dw, dbias
+
+
+def gated_linear(x, w, act: str = "silu", gu=None, out=None, ws=None):
+    """act(x wg^T) * (x wu^T): x [m, hidden], w [2*inter, hidden] (the gate's rows, then the up projection's; bfloat16 or
+    float16) -> [m, inter].  gu [m, 2*inter] is filled with both projections where given: gated_linear_backward reads it."""
+    m, k, inter = x.shape[0], x.shape[-1], w.shape[0] // 2
+    out = torch.empty((m, inter), dtype=x.dtype, device=x.device) if out is None else out
+    if ws is None and moe_gated_linear_workspace(m, inter, k):
+        ws = alloc_gated_linear_workspace(m, inter, k, x.device)
+    moe_gated_linear(x, w, act, gu, out, ws)
+    return out
+
+
+def gated_linear_backward(dh, x, w, gu, act: str = "silu", dx=None, dw=None, ws=None):
+    """(dx, dw) of gated_linear, from gu as it left it."""
+    m, inter, k = dh.shape[0], dh.shape[1], x.shape[-1]
+    dx = torch.empty((m, k), dtype=dh.dtype, device=dh.device) if dx is None else dx
+    dw = torch.empty((2 * inter, k), dtype=dh.dtype, device=dh.device) if dw is None else dw
+    ws = alloc_gated_linear_backward_workspace(m, inter, k, dh.device) if ws is None else ws
+    moe_gated_linear_backward(dh, x, w, gu, act, dx, dw, ws)
+    return dx, dw

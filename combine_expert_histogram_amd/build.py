@@ -12,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,7 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoe_hotpath.so")
 SOURCES = ["api.hip", "layout.hip", "quant.hip", "gemm1.hip", "stage2.hip", "combine.hip",
-           "route_topk.hip", "few_token.hip"]
+           "route_topk.hip", "few_token.hip", "dense.hip", "dense_few.hip", "dense_tile_nt.hip", "dense_tile_nn.hip",
+           "dense_tile_tn.hip", "norm.hip"]
 TRACE_LIB = os.path.join(PKG, "libmoe_hotpath_trace.so")
 CEILING_LIB = os.path.join(PKG, "libmoe_ceiling.so")
 CEILING_SOURCES = ["ceiling.hip"]
@@ -46,25 +48,33 @@ def flags() -> list[str]:
     ]
 
 
-def _link(sources: list[str], out: str, verbose: bool, extra: tuple[str, ...] = ()) -> str:
-    srcs = [os.path.join(CSRC, s) for s in sources]
-    tmp = out + ".tmp"
-    cmd = [hipcc(), *flags(), *extra, *srcs, "-o", tmp]
+def _run(cmd: list[str], verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, out)
+
+
+def _compile(source: str, out: str, verbose: bool, extra: tuple[str, ...] = ()) -> str:
+    _run([hipcc(), *(f for f in flags() if f != "-shared"), *extra, "-c", os.path.join(CSRC, source), "-o", out], verbose)
     return out
 
 
 def build(verbose: bool = False, trace: bool = True) -> str:
-    jobs = [(SOURCES, LIB, verbose), (CEILING_SOURCES, CEILING_LIB, verbose)]
+    libs = [(LIB, SOURCES, ()), (CEILING_LIB, CEILING_SOURCES, ())]
     if trace:
-        jobs.append((SOURCES, TRACE_LIB, verbose, ("-DMOE_TRACE=1",)))
-    with ThreadPoolExecutor(len(jobs)) as pool:      # one hipcc each
-        return [f.result() for f in [pool.submit(_link, *job) for job in jobs]][0]
+        libs.append((TRACE_LIB, SOURCES, ("-DMOE_TRACE=1",)))
+    with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+        # every source of every library by itself, the slow ones first; then one link a library
+        jobs = [(os.path.join(tmp, f"{i}_{s}.o"), s, extra) for i, (_, sources, extra) in enumerate(libs) for s in sources]
+        jobs.sort(key=lambda job: -os.path.getsize(os.path.join(CSRC, job[1])))
+        for f in [pool.submit(_compile, s, out, verbose, extra) for out, s, extra in jobs]:
+            f.result()
+        for i, (lib, sources, _) in enumerate(libs):
+            _run([hipcc(), *flags(), *(os.path.join(tmp, f"{i}_{s}.o") for s in sources), "-o", lib + ".tmp"], verbose)
+            os.replace(lib + ".tmp", lib)
+    return LIB
 
 
 if __name__ == "__main__":

@@ -1,0 +1,221 @@
+// What the dense layers' kernels share: the 16-bit types, the activations, rows that start anywhere, the epilogue of a
+// product, and the launches that the entry points choose from.
+#pragma once
+
+#include "common.h"
+
+namespace moe {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+template <class T>
+struct Vec;
+template <>
+struct Vec<__bf16> {
+    typedef __bf16 x8 __attribute__((ext_vector_type(8)));
+    typedef __bf16 x4 __attribute__((ext_vector_type(4)));
+};
+template <>
+struct Vec<_Float16> {
+    typedef _Float16 x8 __attribute__((ext_vector_type(8)));
+    typedef _Float16 x4 __attribute__((ext_vector_type(4)));
+};
+
+// D += A B over 32 of K, 16 x 16 results: lane l holds row l % 16 of A (column of B), K 8 (l / 16) .. + 7, and results
+// [row 4 (l / 16) + v, column l % 16]
+__device__ __forceinline__ f32x4 mfma(const Vec<__bf16>::x8& a, const Vec<__bf16>::x8& b, const f32x4& c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma(const Vec<_Float16>::x8& a, const Vec<_Float16>::x8& b, const f32x4& c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// Up to eight consecutive elements from anywhere a T may lie; those past n (n <= 8) are zeros.  Whole ones take one
+// 16-byte access, which global memory serves from any address.
+template <class T>
+__device__ __forceinline__ typename Vec<T>::x8 load8(const T* p, int n) {
+    typename Vec<T>::x8 v;
+    if (n >= 8) {
+        __builtin_memcpy(&v, p, 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : (T)0.0f;
+    }
+    return v;
+}
+
+template <class T>
+__device__ __forceinline__ void store8(T* p, const float (&f)[8], int n) {
+    typename Vec<T>::x8 v;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (T)f[i];
+    if (n >= 8) {
+        __builtin_memcpy(p, &v, 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = v[i];
+    }
+}
+
+// ---------------------------------------------------------------- activations
+// In fp32; the exponential and the reciprocal are the hardware's (a few ulps), unseen behind a rounding to 16 bits.
+//   silu      z s(z), s(z) = 1 / (1 + e^-z)
+//   gelu      z P(z), P(z) = erfc(-z / sqrt 2) / 2: no cancellation where z is far below 0
+//   gelu_tanh z (1 + tanh u) / 2 = z s(2u), u = sqrt(2 / pi) (z + 0.044715 z^3)
+__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
+__device__ __forceinline__ float gelu_cdf(float z) { return 0.5f * erfcf(z * -0.70710678118654752f); }
+__device__ __forceinline__ float gelu_tanh_2u(float z) {
+    return z * fmaf(z * z, 2.0f * 0.79788456080286536f * 0.044715f, 2.0f * 0.79788456080286536f);
+}
+
+template <int N>
+__device__ __forceinline__ void activate(float (&z)[N], int act) {
+    switch (act) {
+        case MOE_ACT_RELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) z[i] = z[i] < 0.0f ? 0.0f : z[i];          // NaN stays
+            break;
+        case MOE_ACT_SILU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) z[i] *= sigmoid(z[i]);
+            break;
+        case MOE_ACT_GELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) z[i] *= gelu_cdf(z[i]);
+            break;
+        case MOE_ACT_GELU_TANH:
+#pragma unroll
+            for (int i = 0; i < N; ++i) z[i] *= sigmoid(gelu_tanh_2u(z[i]));
+            break;
+        default: break;
+    }
+}
+
+// a = act(z), d = act'(z)
+template <int N>
+__device__ __forceinline__ void activate_grad(const float (&z)[N], float (&a)[N], float (&d)[N], int act) {
+    switch (act) {
+        case MOE_ACT_RELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                a[i] = z[i] < 0.0f ? 0.0f : z[i];
+                d[i] = z[i] > 0.0f ? 1.0f : 0.0f;
+            }
+            break;
+        case MOE_ACT_SILU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float s = sigmoid(z[i]);
+                a[i] = z[i] * s;
+                d[i] = s * fmaf(z[i], 1.0f - s, 1.0f);
+            }
+            break;
+        case MOE_ACT_GELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float p = gelu_cdf(z[i]);
+                a[i] = z[i] * p;
+                d[i] = fmaf(z[i], 0.39894228040143268f * __expf(-0.5f * z[i] * z[i]), p);
+            }
+            break;
+        case MOE_ACT_GELU_TANH:
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float s = sigmoid(gelu_tanh_2u(z[i]));
+                a[i] = z[i] * s;
+                const float slope = fmaf(z[i] * z[i], 6.0f * 0.79788456080286536f * 0.044715f,
+                                         2.0f * 0.79788456080286536f);
+                const float t = s * (1.0f - s);
+                d[i] = t == 0.0f ? s : fmaf(z[i] * t, slope, s);       // where z^2 overflows, t is 0
+            }
+            break;
+        default:
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                a[i] = z[i];
+                d[i] = 1.0f;
+            }
+    }
+}
+
+// ---------------------------------------------------------------- the epilogue of a product
+// What becomes of the fp32 sums z[row, c]: plain ones, y = act(z + bias) + res; gated ones, y = act(g) u with g and u the
+// columns c and inter + c.  Stored once, rounded once; z (gu) as well where it is not null.
+struct Epilogue {
+    const void* bias;        // [n], null: none
+    const void* res;         // rows of res_ld, null: none; may be y itself
+    void* z;                 // rows of z_ld, null: not kept
+    void* y;                 // rows of y_ld
+    int64_t res_ld, z_ld, y_ld;
+    int n;                   // columns of y
+    int act;
+};
+
+// n <= 8 columns from c of one row
+template <class T>
+__device__ __forceinline__ void finish(const Epilogue& e, int64_t row, int c, float (&v)[8], int n) {
+    if (e.bias) {
+        const typename Vec<T>::x8 b = load8(static_cast<const T*>(e.bias) + c, n);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += (float)b[i];
+    }
+    if (e.z) store8(static_cast<T*>(e.z) + row * e.z_ld + c, v, n);
+    activate(v, e.act);
+    if (e.res) {
+        const typename Vec<T>::x8 r = load8(static_cast<const T*>(e.res) + row * e.res_ld + c, n);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += (float)r[i];
+    }
+    store8(static_cast<T*>(e.y) + row * e.y_ld + c, v, n);
+}
+
+template <class T>
+__device__ __forceinline__ void finish_gated(const Epilogue& e, int64_t row, int c, float (&g)[8], float (&u)[8], int n) {
+    if (e.z) {
+        T* gu = static_cast<T*>(e.z) + row * e.z_ld + c;
+        store8(gu, g, n);
+        store8(gu + e.n, u, n);
+    }
+    activate(g, e.act);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] *= u[i];
+    store8(static_cast<T*>(e.y) + row * e.y_ld + c, g, n);
+}
+
+// ---------------------------------------------------------------- products, as the entry points ask for them
+// C[m, n] = sum_k A(m, k) B(n, k).  A(m, k) at a[m lda + k], or a[k lda + m] where it is transposed; B alike.
+enum Layout { kNT, kNN, kTN };          // forward; dx = dy w (B transposed); dw = dy^T x (both)
+
+struct Product {
+    const void* a;
+    const void* b;
+    int64_t lda, ldb;
+    int m, n, k;             // n: rows of B (gated: 2 inter)
+    int inter;               // gated: columns of y, else 0
+};
+
+struct Plan {
+    int tile;                // 0: few rows, 128: 128 x 128 tiles, 256: 256 x 256 tiles
+    int splits;              // parts of K, summed by a second launch
+    int kper;                // of K to a part, a multiple of kStepK
+};
+constexpr int kStepK = 64;
+
+Plan plan_product(Layout layout, int64_t m, int64_t n, int64_t k, bool aligned);
+int64_t plan_bytes(const Plan& p, int64_t m, int64_t n);          // of fp32 partial sums
+
+bool rows_aligned(const void* p, int64_t ld, int64_t contiguous); // 16-byte rows, whole 16-byte pieces
+
+// one launch each; part: the partial sums where splits > 1
+moe_status launch_tiles(Layout layout, int dtype, bool aligned, const Plan& plan, const Product& p, const Epilogue& e,
+                        float* part, hipStream_t stream);
+moe_status launch_tiles_nt(int dtype, bool aligned, const Plan& plan, const Product& p, const Epilogue& e, float* part,
+                           hipStream_t stream);
+moe_status launch_tiles_nn(int dtype, bool aligned, const Plan& plan, const Product& p, const Epilogue& e, float* part,
+                           hipStream_t stream);
+moe_status launch_tiles_tn(int dtype, bool aligned, const Plan& plan, const Product& p, const Epilogue& e, float* part,
+                           hipStream_t stream);
+moe_status launch_few(int dtype, const Product& p, const Epilogue& e, hipStream_t stream);
+
+}  // namespace moe

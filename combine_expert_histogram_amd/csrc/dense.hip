@@ -1,0 +1,432 @@
+// The dense layers' entry points: which kernels a product takes, the activations' gradients, and the sums over parts.
+#include "dense.h"
+
+namespace moe {
+
+bool rows_aligned(const void* p, int64_t ld, int64_t contiguous) {
+    return ((uintptr_t)p & 15) == 0 && ld % 8 == 0 && contiguous % 8 == 0;
+}
+
+Plan plan_product(Layout layout, int64_t m, int64_t n, int64_t k, bool aligned) {
+    if (layout == kNT && m <= 64) return Plan{0, 1, (int)((k + kStepK - 1) / kStepK * kStepK)};
+    const auto tiles = [&](int64_t t) { return ((m + t - 1) / t) * ((n + t - 1) / t); };
+    Plan p{128, 1, 0};
+    int64_t slots = 512, most = tiles(128);
+    if (aligned && tiles(256) >= 192) p.tile = 256, slots = 256, most = tiles(256);
+    const int64_t steps = (k + kStepK - 1) / kStepK;
+    int64_t splits = std::min(slots / std::max<int64_t>(most, 1), steps / 8);
+    splits = std::max<int64_t>(1, std::min<int64_t>(splits, 32));
+    const int64_t per = (steps + splits - 1) / splits;
+    p.kper = (int)(per * kStepK);
+    p.splits = (int)((steps + per - 1) / per);
+    return p;
+}
+
+int64_t plan_bytes(const Plan& p, int64_t m, int64_t n) {
+    return p.splits > 1 ? (p.splits * m * n * 4 + 255) & ~int64_t(255) : 0;
+}
+
+moe_status launch_tiles(Layout layout, int dtype, bool aligned, const Plan& plan, const Product& p, const Epilogue& e,
+                        float* part, hipStream_t stream) {
+    if (layout == kNT) return launch_tiles_nt(dtype, aligned, plan, p, e, part, stream);
+    if (layout == kNN) return launch_tiles_nn(dtype, aligned, plan, p, e, part, stream);
+    return launch_tiles_tn(dtype, aligned, plan, p, e, part, stream);
+}
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// ---------------------------------------------------------------- the parts of K summed, then the epilogue
+struct JoinArgs {
+    const float* part;
+    int64_t step;            // floats of one part
+    int64_t items;
+    int splits, n, chunks, inter;
+    Epilogue e;
+};
+
+__device__ __forceinline__ void add_parts(const JoinArgs& t, int64_t at, float (&v)[8], int n) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    for (int s = 0; s < t.splits; ++s) {
+        const float* p = t.part + s * t.step + at;
+        if (n >= 8) {
+            float f[8];
+            __builtin_memcpy(f, p, 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += f[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < n) v[i] += p[i];
+        }
+    }
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads) join_kernel(JoinArgs t) {
+    for (int64_t item = (int64_t)blockIdx.x * kThreads + threadIdx.x; item < t.items; item += (int64_t)gridDim.x * kThreads) {
+        const int64_t row = item / t.chunks;
+        const int c = (int)(item - row * t.chunks) * 8;
+        const int n = min(8, t.e.n - c);
+        float v[8], u[8];
+        add_parts(t, row * t.n + c, v, n);
+        if (t.inter) {
+            add_parts(t, row * t.n + t.inter + c, u, n);
+            finish_gated<T>(t.e, row, c, v, u, n);
+        } else {
+            finish<T>(t.e, row, c, v, n);
+        }
+    }
+}
+
+int grid_of(int64_t items) { return (int)std::min<int64_t>((items + kThreads - 1) / kThreads, 16384); }
+
+moe_status run_product(Layout layout, int dtype, bool aligned, const Product& p, const Epilogue& e, void* ws,
+                       hipStream_t stream) {
+    const Plan plan = plan_product(layout, p.m, p.inter ? p.inter * 2 : p.n, p.k, aligned);
+    if (plan.tile == 0) return launch_few(dtype, p, e, stream);
+    float* part = static_cast<float*>(ws);
+    moe_status st = launch_tiles(layout, dtype, aligned, plan, p, e, part, stream);
+    if (st != MOE_OK || plan.splits == 1) return st;
+    JoinArgs t;
+    t.part = part, t.step = (int64_t)p.m * p.n, t.splits = plan.splits, t.n = p.n, t.inter = p.inter, t.e = e;
+    t.chunks = (e.n + 7) / 8;
+    t.items = (int64_t)p.m * t.chunks;
+    if (dtype == MOE_BF16) hipLaunchKernelGGL(join_kernel<__bf16>, dim3(grid_of(t.items)), dim3(kThreads), 0, stream, t);
+    else hipLaunchKernelGGL(join_kernel<_Float16>, dim3(grid_of(t.items)), dim3(kThreads), 0, stream, t);
+    return launch_status();
+}
+
+// ---------------------------------------------------------------- the activations' gradients
+// d[row, :] = [dh u act'(g), dh act(g)]: read and written once, 8 columns of a row to a thread
+struct GateGradArgs {
+    const void* dh;
+    const void* gu;
+    void* d;
+    int64_t dh_ld, gu_ld, d_ld, items;
+    int inter, chunks, act;
+};
+
+template <class T>
+__global__ void __launch_bounds__(kThreads) gate_grad_kernel(GateGradArgs t) {
+    for (int64_t item = (int64_t)blockIdx.x * kThreads + threadIdx.x; item < t.items; item += (int64_t)gridDim.x * kThreads) {
+        const int64_t row = item / t.chunks;
+        const int c = (int)(item - row * t.chunks) * 8, n = min(8, t.inter - c);
+        const T* gu = static_cast<const T*>(t.gu) + row * t.gu_ld + c;
+        const auto dh = load8(static_cast<const T*>(t.dh) + row * t.dh_ld + c, n);
+        const auto gv = load8(gu, n), uv = load8(gu + t.inter, n);
+        float g[8], a[8], d[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = (float)gv[i];
+        activate_grad(g, a, d, t.act);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            d[i] *= (float)dh[i] * (float)uv[i];
+            a[i] *= (float)dh[i];
+        }
+        T* to = static_cast<T*>(t.d) + row * t.d_ld + c;
+        store8(to, d, n);
+        store8(to + t.inter, a, n);
+    }
+}
+
+// dz = dy act'(z), kept for the products where `d` is not null, and its column sums over this workgroup's rows: a
+// workgroup takes 256 columns (8 to a thread) and every eighth row of its share to one of its eight groups of threads
+constexpr int kColumns = 256, kRowGroups = kThreads * 8 / kColumns, kMaxRowParts = 128;
+
+struct DzArgs {
+    const void* dy;
+    const void* z;           // null: no activation
+    void* d;                 // null: not kept
+    float* sums;             // [gridDim.y, n], null: not wanted
+    int64_t dy_ld, z_ld, d_ld, m, rows;
+    int n, act;
+};
+
+template <class T>
+__global__ void __launch_bounds__(kThreads) dz_kernel(DzArgs t) {
+    __shared__ float lds[kRowGroups][kColumns + 4];
+    const int c = blockIdx.x * kColumns + (threadIdx.x % (kColumns / 8)) * 8, group = threadIdx.x / (kColumns / 8);
+    const int n = min(8, t.n - c);
+    const int64_t first = blockIdx.y * t.rows, last = min(t.m, first + t.rows);
+    float sum[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
+    if (n > 0) {
+        for (int64_t row = first + group; row < last; row += kRowGroups) {
+            const auto dy = load8(static_cast<const T*>(t.dy) + row * t.dy_ld + c, n);
+            float d[8];
+            if (t.z) {
+                const auto zv = load8(static_cast<const T*>(t.z) + row * t.z_ld + c, n);
+                float z[8], a[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z[i] = (float)zv[i];
+                activate_grad(z, a, d, t.act);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[i] *= (float)dy[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[i] = (float)dy[i];
+            }
+            if (t.d) store8(static_cast<T*>(t.d) + row * t.d_ld + c, d, n);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] += d[i];
+        }
+    }
+    if (!t.sums) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) lds[group][(threadIdx.x % (kColumns / 8)) * 8 + i] = sum[i];
+    __syncthreads();
+    const int col = blockIdx.x * kColumns + threadIdx.x;
+    if (col >= t.n) return;
+    float s = 0.0f;
+#pragma unroll
+    for (int g = 0; g < kRowGroups; ++g) s += lds[g][threadIdx.x];
+    t.sums[(int64_t)blockIdx.y * t.n + col] = s;
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads) column_sum_kernel(const float* sums, int parts, int n, void* out) {
+    const int c = blockIdx.x * kThreads + threadIdx.x;
+    if (c >= n) return;
+    float s = 0.0f;
+    for (int p = 0; p < parts; ++p) s += sums[(int64_t)p * n + c];
+    static_cast<T*>(out)[c] = (T)s;
+}
+
+int64_t row_parts(int64_t m) { return std::max<int64_t>(1, std::min<int64_t>((m + 63) / 64, kMaxRowParts)); }
+
+template <class T>
+moe_status launch_dz(DzArgs t, void* dbias, hipStream_t stream) {
+    const int64_t parts = row_parts(t.m);
+    t.rows = (t.m + parts - 1) / parts;
+    hipLaunchKernelGGL(dz_kernel<T>, dim3((t.n + kColumns - 1) / kColumns, (int)parts), dim3(kThreads), 0, stream, t);
+    moe_status st = launch_status();
+    if (st != MOE_OK || !dbias) return st;
+    hipLaunchKernelGGL(column_sum_kernel<T>, dim3((t.n + kThreads - 1) / kThreads), dim3(kThreads), 0, stream, t.sums,
+                       (int)parts, t.n, dbias);
+    return launch_status();
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads) zero_rows_kernel(T* p, int64_t ld, int cols, int64_t items) {
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < items; i += (int64_t)gridDim.x * kThreads)
+        p[i / cols * ld + i % cols] = (T)0.0f;
+}
+
+moe_status zero_rows(void* p, int64_t ld, int64_t rows, int cols, hipStream_t stream) {
+    const int64_t items = rows * cols;
+    hipLaunchKernelGGL(zero_rows_kernel<_Float16>, dim3(grid_of(items)), dim3(kThreads), 0, stream,
+                       static_cast<_Float16*>(p), ld, cols, items);        // +0 in either type
+    return launch_status();
+}
+
+// ---------------------------------------------------------------- checks and sizes
+int64_t pad(int64_t bytes) { return (bytes + 255) & ~int64_t(255); }
+int64_t pad8(int64_t n) { return (n + 7) & ~int64_t(7); }
+
+bool bad_dtype(int dtype) { return dtype != MOE_BF16 && dtype != MOE_FP16; }
+bool bad_act(int act) { return act < MOE_ACT_NONE || act > MOE_ACT_GELU_TANH; }
+bool misplaced(const void* p, size_t to) { return ((uintptr_t)p & (to - 1)) != 0; }
+// a matrix of rows of `cols` elements
+bool bad_rows(const void* p, int64_t ld, int64_t cols) { return !p || misplaced(p, 2) || ld < cols; }
+constexpr int64_t kMaxLd = 1 << 22, kMaxElements = (int64_t)1 << 40;
+
+moe_status check_sizes(int64_t m, int64_t n, int64_t k) {
+    if (m < 0 || n < 1 || k < 1) return MOE_ERR_INVALID_ARG;
+    if (m * n >= kMaxElements || m * k >= kMaxElements || n * k >= kMaxElements ||
+        std::max({m, n, k}) >= (1 << 30))
+        return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+int64_t product_bytes(Layout layout, int64_t m, int64_t n, int64_t k) {
+    return std::max(plan_bytes(plan_product(layout, m, n, k, true), m, n),
+                    plan_bytes(plan_product(layout, m, n, k, false), m, n));
+}
+
+// the backward passes' workspace: dz (or [dg du]), the bias's column sums, and the products' parts
+struct Backward {
+    int64_t sums, parts, bytes;
+};
+Backward backward_of(int64_t m, int64_t n, int64_t k, bool keeps) {
+    Backward b;
+    b.sums = keeps ? pad(m * pad8(n) * 2) : 0;
+    b.parts = b.sums + pad(row_parts(m) * n * 4);
+    b.bytes = b.parts + std::max(product_bytes(kNN, m, k, n), product_bytes(kTN, n, k, m));
+    return b;
+}
+
+// dx = d w and dw = d^T x, either of them left out where it is null
+moe_status run_backward(int64_t m, int64_t n, int64_t k, int dtype, const void* d, int64_t d_ld, const void* x, int64_t x_ld,
+                        const void* w, int64_t w_ld, void* dx, int64_t dx_ld, void* dw, int64_t dw_ld, void* ws,
+                        hipStream_t stream) {
+    moe_status st = MOE_OK;
+    if (dx) {
+        const Product p{d, w, d_ld, w_ld, (int)m, (int)k, (int)n, 0};
+        const Epilogue e{nullptr, nullptr, nullptr, dx, 0, 0, dx_ld, (int)k, MOE_ACT_NONE};
+        st = run_product(kNN, dtype, rows_aligned(d, d_ld, n) && rows_aligned(w, w_ld, k), p, e, ws, stream);
+    }
+    if (dw && st == MOE_OK) {
+        const Product p{d, x, d_ld, x_ld, (int)n, (int)k, (int)m, 0};
+        const Epilogue e{nullptr, nullptr, nullptr, dw, 0, 0, dw_ld, (int)k, MOE_ACT_NONE};
+        st = run_product(kTN, dtype, rows_aligned(d, d_ld, n) && rows_aligned(x, x_ld, k), p, e, ws, stream);
+    }
+    return st;
+}
+
+bool wide(int64_t a, int64_t b, int64_t c, int64_t d, int64_t e) {
+    return std::max({a, b, c, d, e}) >= kMaxLd;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_linear_workspace(int32_t m, int32_t n, int32_t k, size_t* bytes) {
+    const moe_status st = check_sizes(m, n, k);
+    if (st != MOE_OK) return st;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = (size_t)product_bytes(kNT, m, n, k);
+    return MOE_OK;
+}
+
+extern "C" moe_status moe_linear(int32_t m, int32_t n, int32_t k, int32_t dtype, const void* x, int64_t x_stride,
+                                 const void* w, int64_t w_stride, const void* bias, int32_t act, const void* residual,
+                                 int64_t residual_stride, void* z, int64_t z_stride, void* y, int64_t y_stride, void* ws,
+                                 size_t ws_bytes, void* hip_stream) {
+    const moe_status st = check_sizes(m, n, k);
+    if (st != MOE_OK) return st;
+    if (bad_dtype(dtype) || bad_act(act)) return MOE_ERR_INVALID_ARG;
+    if (m == 0) return MOE_OK;
+    if (bad_rows(x, x_stride, k) || bad_rows(w, w_stride, k) || bad_rows(y, y_stride, n) || misplaced(bias, 2) ||
+        (residual && bad_rows(residual, residual_stride, n)) || (z && bad_rows(z, z_stride, n)))
+        return MOE_ERR_INVALID_ARG;
+    if (wide(x_stride, w_stride, y_stride, residual ? residual_stride : 0, z ? z_stride : 0)) return MOE_ERR_UNSUPPORTED;
+    const int64_t need = product_bytes(kNT, m, n, k);
+    if (need && (!ws || ws_bytes < (size_t)need)) return MOE_ERR_WORKSPACE;
+    if (need && misplaced(ws, 16)) return MOE_ERR_INVALID_ARG;
+    const Product p{x, w, x_stride, w_stride, m, n, k, 0};
+    const Epilogue e{bias, residual, z, y, residual_stride, z_stride, y_stride, n, act};
+    return run_product(kNT, dtype, rows_aligned(x, x_stride, k) && rows_aligned(w, w_stride, k), p, e, ws,
+                       reinterpret_cast<hipStream_t>(hip_stream));
+}
+
+extern "C" moe_status moe_linear_backward_workspace(int32_t m, int32_t n, int32_t k, int32_t act, size_t* bytes) {
+    const moe_status st = check_sizes(m, n, k);
+    if (st != MOE_OK) return st;
+    if (!bytes || bad_act(act)) return MOE_ERR_INVALID_ARG;
+    *bytes = (size_t)backward_of(m, n, k, act != MOE_ACT_NONE).bytes;
+    return MOE_OK;
+}
+
+extern "C" moe_status moe_linear_backward(int32_t m, int32_t n, int32_t k, int32_t dtype, const void* dy, int64_t dy_stride,
+                                          const void* x, int64_t x_stride, const void* w, int64_t w_stride, int32_t act,
+                                          const void* z, int64_t z_stride, void* dx, int64_t dx_stride, void* dw,
+                                          int64_t dw_stride, void* dbias, void* ws, size_t ws_bytes, void* hip_stream) {
+    moe_status st = check_sizes(m, n, k);
+    if (st != MOE_OK) return st;
+    if (bad_dtype(dtype) || bad_act(act)) return MOE_ERR_INVALID_ARG;
+    const bool keeps = act != MOE_ACT_NONE;
+    const hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
+    if ((dw && bad_rows(dw, dw_stride, k)) || misplaced(dbias, 2)) return MOE_ERR_INVALID_ARG;
+    if (m == 0) {
+        if (dw) st = zero_rows(dw, dw_stride, n, k, stream);
+        if (dbias && st == MOE_OK) st = zero_rows(dbias, n, 1, n, stream);
+        return st;
+    }
+    if (bad_rows(dy, dy_stride, n) || (keeps && bad_rows(z, z_stride, n)) || (dw && bad_rows(x, x_stride, k)) ||
+        (dx && (bad_rows(w, w_stride, k) || bad_rows(dx, dx_stride, k))))
+        return MOE_ERR_INVALID_ARG;
+    if (wide(dy_stride, dw ? std::max(x_stride, dw_stride) : 0, dx ? std::max(w_stride, dx_stride) : 0,
+             keeps ? std::max(z_stride, pad8(n)) : 0, 0))
+        return MOE_ERR_UNSUPPORTED;
+    if (!dx && !dw && !dbias) return MOE_OK;
+    const Backward b = backward_of(m, n, k, keeps);
+    if (!ws || ws_bytes < (size_t)b.bytes) return MOE_ERR_WORKSPACE;
+    if (misplaced(ws, 16)) return MOE_ERR_INVALID_ARG;
+    uint8_t* at = static_cast<uint8_t*>(ws);
+    const void* d = dy;
+    int64_t d_ld = dy_stride;
+    if (keeps || dbias) {
+        const bool kept = keeps && (dx || dw);
+        const DzArgs t{dy, keeps ? z : nullptr, kept ? at : nullptr, dbias ? reinterpret_cast<float*>(at + b.sums) : nullptr,
+                       dy_stride, z_stride, pad8(n), m, 0, n, act};
+        st = dtype == MOE_BF16 ? launch_dz<__bf16>(t, dbias, stream) : launch_dz<_Float16>(t, dbias, stream);
+        if (st != MOE_OK) return st;
+        if (kept) d = at, d_ld = pad8(n);
+    }
+    return run_backward(m, n, k, dtype, d, d_ld, x, x_stride, w, w_stride, dx, dx_stride, dw, dw_stride, at + b.parts, stream);
+}
+
+extern "C" moe_status moe_gated_linear_workspace(int32_t m, int32_t inter, int32_t hidden, size_t* bytes) {
+    const moe_status st = check_sizes(m, inter < 1 ? inter : 2 * (int64_t)inter, hidden);
+    if (st != MOE_OK) return st;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = (size_t)product_bytes(kNT, m, 2 * (int64_t)inter, hidden);
+    return MOE_OK;
+}
+
+extern "C" moe_status moe_gated_linear(int32_t m, int32_t inter, int32_t hidden, int32_t dtype, const void* x,
+                                       int64_t x_stride, const void* w, int64_t w_stride, int32_t act, void* gu,
+                                       int64_t gu_stride, void* h, int64_t h_stride, void* ws, size_t ws_bytes,
+                                       void* hip_stream) {
+    const int64_t n = 2 * (int64_t)inter;
+    const moe_status st = check_sizes(m, n, hidden);
+    if (st != MOE_OK) return st;
+    if (bad_dtype(dtype) || bad_act(act)) return MOE_ERR_INVALID_ARG;
+    if (m == 0) return MOE_OK;
+    if (bad_rows(x, x_stride, hidden) || bad_rows(w, w_stride, hidden) || bad_rows(h, h_stride, inter) ||
+        (gu && bad_rows(gu, gu_stride, n)))
+        return MOE_ERR_INVALID_ARG;
+    if (wide(x_stride, w_stride, h_stride, gu ? gu_stride : 0, 0)) return MOE_ERR_UNSUPPORTED;
+    const int64_t need = product_bytes(kNT, m, n, hidden);
+    if (need && (!ws || ws_bytes < (size_t)need)) return MOE_ERR_WORKSPACE;
+    if (need && misplaced(ws, 16)) return MOE_ERR_INVALID_ARG;
+    const Product p{x, w, x_stride, w_stride, m, (int)n, hidden, inter};
+    const Epilogue e{nullptr, nullptr, gu, h, 0, gu_stride, h_stride, inter, act};
+    return run_product(kNT, dtype, rows_aligned(x, x_stride, hidden) && rows_aligned(w, w_stride, hidden), p, e, ws,
+                       reinterpret_cast<hipStream_t>(hip_stream));
+}
+
+extern "C" moe_status moe_gated_linear_backward_workspace(int32_t m, int32_t inter, int32_t hidden, size_t* bytes) {
+    const moe_status st = check_sizes(m, inter < 1 ? inter : 2 * (int64_t)inter, hidden);
+    if (st != MOE_OK) return st;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = (size_t)backward_of(m, 2 * (int64_t)inter, hidden, true).bytes;
+    return MOE_OK;
+}
+
+extern "C" moe_status moe_gated_linear_backward(int32_t m, int32_t inter, int32_t hidden, int32_t dtype, const void* dh,
+                                                int64_t dh_stride, const void* gu, int64_t gu_stride, const void* x,
+                                                int64_t x_stride, const void* w, int64_t w_stride, int32_t act, void* dx,
+                                                int64_t dx_stride, void* dw, int64_t dw_stride, void* ws, size_t ws_bytes,
+                                                void* hip_stream) {
+    const int64_t n = 2 * (int64_t)inter;
+    moe_status st = check_sizes(m, n, hidden);
+    if (st != MOE_OK) return st;
+    if (bad_dtype(dtype) || bad_act(act)) return MOE_ERR_INVALID_ARG;
+    const hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
+    if (dw && bad_rows(dw, dw_stride, hidden)) return MOE_ERR_INVALID_ARG;
+    if (m == 0) return dw ? zero_rows(dw, dw_stride, n, hidden, stream) : MOE_OK;
+    if (bad_rows(dh, dh_stride, inter) || bad_rows(gu, gu_stride, n) || (dw && bad_rows(x, x_stride, hidden)) ||
+        (dx && (bad_rows(w, w_stride, hidden) || bad_rows(dx, dx_stride, hidden))))
+        return MOE_ERR_INVALID_ARG;
+    if (wide(dh_stride, gu_stride, dw ? std::max(x_stride, dw_stride) : 0, dx ? std::max(w_stride, dx_stride) : 0, pad8(n)))
+        return MOE_ERR_UNSUPPORTED;
+    if (!dx && !dw) return MOE_OK;
+    const Backward b = backward_of(m, n, hidden, true);
+    if (!ws || ws_bytes < (size_t)b.bytes) return MOE_ERR_WORKSPACE;
+    if (misplaced(ws, 16)) return MOE_ERR_INVALID_ARG;
+    uint8_t* at = static_cast<uint8_t*>(ws);
+    GateGradArgs t{dh, gu, at, dh_stride, gu_stride, pad8(n), 0, inter, (inter + 7) / 8, act};
+    t.items = (int64_t)m * t.chunks;
+    if (dtype == MOE_BF16) hipLaunchKernelGGL(gate_grad_kernel<__bf16>, dim3(grid_of(t.items)), dim3(kThreads), 0, stream, t);
+    else hipLaunchKernelGGL(gate_grad_kernel<_Float16>, dim3(grid_of(t.items)), dim3(kThreads), 0, stream, t);
+    if ((st = launch_status()) != MOE_OK) return st;
+    return run_backward(m, n, hidden, dtype, at, pad8(n), x, x_stride, w, w_stride, dx, dx_stride, dw, dw_stride, at + b.parts,
+                        stream);
+}

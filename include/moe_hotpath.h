@@ -456,6 +456,150 @@ moe_status moe_few_token_layer(const moe_dims* dims, int32_t inter, const uint16
                                const moe_weight* w2, uint16_t* out_bf16, void* ws, size_t ws_bytes,
                                void* hip_stream);
 
+/*
+ * The dense half of an MoE block, in the model's own 16-bit type, forward and
+ * backward: the norm in front of router and experts, the shared (dense)
+ * expert's gate and up projections with their activation, and the linear layer
+ * (its down projection, added to moe_combine's output; a router; any other).
+ * A block of them:
+ *     n = moe_layer_norm(x);  h = moe_gated_linear(n, w1);
+ *     y = moe_linear(h, w2, residual = moe_combine(...))
+ * Rows are tokens.  Row i of a matrix starts i strides (in elements) after row
+ * 0; its elements are contiguous, and what lies between the rows is neither
+ * read nor written.  Any stride of at least the row's length, any size of 1 and
+ * more and any alignment of the type is taken; rows that start on 16-byte
+ * boundaries and are whole 16 bytes long are the fast ones.  No output overlaps
+ * an input, another output or ws, but where said.  Calls with no rows write
+ * nothing, and the gradients of the weights are zeros.  Sums and statistics are
+ * fp32; every output is rounded once, to nearest even.  Sums have a fixed order:
+ * the same call gives the same bits.
+ */
+typedef enum moe_dtype {
+    MOE_BF16 = 0,
+    MOE_FP16 = 1,
+    MOE_FP32 = 2                /* the norm only                               */
+} moe_dtype;
+
+typedef enum moe_act {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_RELU = 1,           /* max(z, 0); its derivative at 0 is 0         */
+    MOE_ACT_SILU = 2,           /* z / (1 + e^-z)                              */
+    MOE_ACT_GELU = 3,           /* z (1 + erf(z / sqrt 2)) / 2                 */
+    MOE_ACT_GELU_TANH = 4       /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+} moe_act;
+
+/*
+ * moe_layer_norm: for each row i < rows,
+ *   mean = sum_j x / cols;  rstd = 1 / sqrt(sum_j (x - mean)^2 / cols + eps);
+ *   y = (x - mean) * rstd * weight + bias
+ * In:  x [rows, cols] of dtype;  weight, bias [cols] of param_dtype (dtype or
+ *      MOE_FP32), weight NULL: ones, bias NULL: zeros;  eps >= 0.
+ * Out: y [rows, cols] of dtype (may be x itself, with x's stride);  mean, rstd
+ *      float32 [rows], each NULL if not wanted (the backward pass reads both).
+ * A row with an infinity or a NaN gives NaNs in that row alone.
+ */
+moe_status moe_layer_norm(int32_t rows, int32_t cols, int32_t dtype, int32_t param_dtype,
+                          const void* x, int64_t x_stride, const void* weight, const void* bias,
+                          float eps, void* y, int64_t y_stride, float* mean, float* rstd,
+                          void* hip_stream);
+
+/* Workspace bytes moe_layer_norm_backward needs (host-only): the weight and
+ * bias gradients' partial sums. */
+moe_status moe_layer_norm_backward_workspace(int32_t rows, int32_t cols, size_t* bytes);
+
+/*
+ * moe_layer_norm_backward: with n = (x - mean) * rstd and g = dy * weight,
+ *   dx = rstd * (g - sum_j g / cols - n * sum_j (g * n) / cols)
+ *   dweight = sum_i dy * n;  dbias = sum_i dy
+ * In:  dy, x [rows, cols] of dtype;  weight as above;  mean, rstd float32 [rows].
+ * Out: dx [rows, cols] of dtype (may be dy or x itself, with its stride);
+ *      dweight, dbias [cols] of param_dtype;  each NULL if not wanted.
+ * ws: at least moe_layer_norm_backward_workspace bytes, 16-byte aligned, no
+ * initialisation; not read if neither dweight nor dbias is wanted.
+ */
+moe_status moe_layer_norm_backward(int32_t rows, int32_t cols, int32_t dtype, int32_t param_dtype,
+                                   const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                                   const void* weight, const float* mean, const float* rstd,
+                                   void* dx, int64_t dx_stride, void* dweight, void* dbias,
+                                   void* ws, size_t ws_bytes, void* hip_stream);
+
+/* Workspace bytes moe_linear needs (host-only; may be 0): the fp32 sums of the
+ * parts that K is cut into where there are few tiles. */
+moe_status moe_linear_workspace(int32_t m, int32_t n, int32_t k, size_t* bytes);
+
+/*
+ * moe_linear: z = x w^T + bias;  y = act(z) + residual, for m rows.
+ * In:  x [m, k], w [n, k], bias [n] (NULL: none), residual [m, n] (NULL: none;
+ *      may be y itself, with y's stride), all of dtype (MOE_BF16 or MOE_FP16).
+ * Out: y [m, n];  z [m, n] if not NULL (moe_linear_backward reads it), of dtype;
+ *      act and residual are taken on the fp32 value, not on the rounded z.
+ * ws: at least moe_linear_workspace bytes, 16-byte aligned, no initialisation
+ * (may be NULL if that is 0).  Strides below 2^22, m * n and m * k and n * k
+ * below 2^40, else MOE_ERR_UNSUPPORTED (in all four products' calls).
+ */
+moe_status moe_linear(int32_t m, int32_t n, int32_t k, int32_t dtype, const void* x, int64_t x_stride,
+                      const void* w, int64_t w_stride, const void* bias, int32_t act,
+                      const void* residual, int64_t residual_stride, void* z, int64_t z_stride,
+                      void* y, int64_t y_stride, void* ws, size_t ws_bytes, void* hip_stream);
+
+/* Workspace bytes moe_linear_backward needs (host-only): dz where there is an
+ * activation, partial sums of the products and of dbias. */
+moe_status moe_linear_backward_workspace(int32_t m, int32_t n, int32_t k, int32_t act, size_t* bytes);
+
+/*
+ * moe_linear_backward: dz = dy * act'(z);  dx = dz w;  dw = dz^T x;
+ * dbias = sum_i dz  (the residual's gradient is dy).
+ * In:  dy, z [m, n] (z not read, and may be NULL, for MOE_ACT_NONE);  x [m, k],
+ *      w [n, k] (x is not read if dw is not wanted, nor w if dx is not; NULL
+ *      then).
+ * Out: dx [m, k], dw [n, k], dbias [n], of dtype;  each NULL if not wanted.
+ * dz is rounded to dtype for the two products (their matrix instructions take
+ * 16 bits); dbias sums it in fp32.
+ * ws: at least moe_linear_backward_workspace bytes, 16-byte aligned, no
+ * initialisation.
+ */
+moe_status moe_linear_backward(int32_t m, int32_t n, int32_t k, int32_t dtype, const void* dy, int64_t dy_stride,
+                               const void* x, int64_t x_stride, const void* w, int64_t w_stride,
+                               int32_t act, const void* z, int64_t z_stride, void* dx, int64_t dx_stride,
+                               void* dw, int64_t dw_stride, void* dbias, void* ws, size_t ws_bytes,
+                               void* hip_stream);
+
+/* Workspace bytes moe_gated_linear needs (host-only; may be 0). */
+moe_status moe_gated_linear_workspace(int32_t m, int32_t inter, int32_t hidden, size_t* bytes);
+
+/*
+ * moe_gated_linear: g = x wg^T;  u = x wu^T;  h = act(g) * u, for m rows, both
+ * projections in one pass over x.
+ * In:  x [m, hidden];  w [2*inter, hidden], wg its first inter rows and wu the
+ *      rest (the experts' w1), of dtype (MOE_BF16 or MOE_FP16).
+ * Out: h [m, inter];  gu [m, 2*inter] (g, then u) if not NULL
+ *      (moe_gated_linear_backward reads it);  h is made of the fp32 g and u.
+ * ws: at least moe_gated_linear_workspace bytes, as moe_linear's.
+ */
+moe_status moe_gated_linear(int32_t m, int32_t inter, int32_t hidden, int32_t dtype,
+                            const void* x, int64_t x_stride, const void* w, int64_t w_stride, int32_t act,
+                            void* gu, int64_t gu_stride, void* h, int64_t h_stride,
+                            void* ws, size_t ws_bytes, void* hip_stream);
+
+/* Workspace bytes moe_gated_linear_backward needs (host-only). */
+moe_status moe_gated_linear_backward_workspace(int32_t m, int32_t inter, int32_t hidden, size_t* bytes);
+
+/*
+ * moe_gated_linear_backward: dg = dh * u * act'(g);  du = dh * act(g);
+ * dx = dg wg + du wu;  dw = [dg du]^T x.
+ * In:  dh [m, inter];  gu [m, 2*inter] as kept;  x, w as above (x is not read
+ *      if dw is not wanted, nor w if dx is not; NULL then).
+ * Out: dx [m, hidden], dw [2*inter, hidden], of dtype;  each NULL if not wanted.
+ * dg and du are rounded to dtype for the two products.
+ * ws: at least moe_gated_linear_backward_workspace bytes, 16-byte aligned, no
+ * initialisation.
+ */
+moe_status moe_gated_linear_backward(int32_t m, int32_t inter, int32_t hidden, int32_t dtype,
+                                     const void* dh, int64_t dh_stride, const void* gu, int64_t gu_stride,
+                                     const void* x, int64_t x_stride, const void* w, int64_t w_stride,
+                                     int32_t act, void* dx, int64_t dx_stride, void* dw, int64_t dw_stride,
+                                     void* ws, size_t ws_bytes, void* hip_stream);
+
 #ifdef __cplusplus
 }
 #endif

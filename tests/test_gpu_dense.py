@@ -1,0 +1,194 @@
+"""GPU: the linear and gated linear layers, forward and backward, against float64.  Whole-numbered inputs make every sum
+exact, so those tests ask for the exact result rounded once, bit for bit; the others hold bounds that count roundings."""
+import math
+
+import pytest
+import torch
+
+import combine_expert_histogram_amd as moe
+from dense_helpers import (ACTS, HALF, Output, act64, act_error, close, generator, grad_error, ids, inside, integers,
+                           linear_sizes, normal, rounding, same, sum_error)
+from gpu_helpers import require_gpu, say
+
+pytestmark = pytest.mark.gpu
+
+# how the matrices lie: (elements before a row, after it); (0, 0) takes what rows of whole 16 bytes allow
+PLACES = [(0, 0), (8, 16), (0, 3), (1, 0)]
+
+
+def placed(t, place):
+    return t if place == (0, 0) else inside(t, place[1], place[0])
+
+
+@pytest.mark.parametrize("dtype", HALF, ids=ids)
+@pytest.mark.parametrize("place", PLACES, ids=ids)
+@pytest.mark.parametrize("size", linear_sizes(), ids=ids)
+def test_linear_exact(size, place, dtype):
+    require_gpu()
+    m, n, k = size
+    say(f"linear {size} {place} {dtype}")
+    g = generator(m + 10 * n + 100 * k)
+    x, w = integers(g, m, k, dtype), integers(g, n, k, dtype)
+    bias, res = integers(g, 1, n, dtype, 9)[0], integers(g, m, n, dtype, 9)
+    z64 = x.double() @ w.double().T
+    y, z = Output(m, n, dtype, place[1], place[0]), Output(m, n, dtype, place[0], place[1])
+    xp, wp = placed(x, place), placed(w, place)
+    moe.linear(xp, wp, out=y.view)
+    same(y.view, z64, "plain")
+    moe.linear(xp, wp, bias=bias, act="relu", residual=placed(res, place), z=z.view, out=y.view)
+    same(z.view, z64 + bias.double(), "z")
+    same(y.view, act64(z64 + bias.double(), "relu")[0] + res.double(), "y")
+    y.check_surroundings()
+    z.check_surroundings()
+
+
+@pytest.mark.parametrize("dtype", HALF, ids=ids)
+@pytest.mark.parametrize("place", PLACES, ids=ids)
+@pytest.mark.parametrize("size", linear_sizes(), ids=ids)
+def test_linear_backward_exact(size, place, dtype):
+    require_gpu()
+    m, n, k = size
+    say(f"linear backward {size} {place} {dtype}")
+    g = generator(m + 10 * n + 100 * k + 1)
+    x, w, dy = integers(g, m, k, dtype), integers(g, n, k, dtype), integers(g, m, n, dtype)
+    z = integers(g, m, n, dtype, 2)
+    dx, dw = Output(m, k, dtype, place[1], place[0]), Output(n, k, dtype, place[0], place[1])
+    xp, wp, dyp = placed(x, place), placed(w, place), placed(dy, place)
+    for act in ("none", "relu"):
+        dz = dy.double() * act64(z.double(), act)[1]
+        _, _, db = moe.linear_backward(dyp, xp, wp, act=act, z=None if act == "none" else placed(z, place), dx=dx.view,
+                                       dw=dw.view)
+        same(dx.view, dz @ w.double(), act + " dx")
+        same(dw.view, dz.T @ x.double(), act + " dw")
+        same(db, dz.sum(0), act + " dbias")
+    dx.check_surroundings()
+    dw.check_surroundings()
+
+
+def gated_sizes():
+    return [(1, 1, 1), (1, 8, 8), (1, 2048, 7168), (2, 9, 65), (16, 64, 128), (17, 100, 1000), (33, 17, 127), (64, 136, 520),
+            (65, 8, 8), (66, 31, 72), (100, 1, 37), (127, 65, 63), (128, 64, 64), (129, 72, 65), (200, 200, 1160),
+            (256, 128, 2048), (70, 40, 8200), (300, 517, 257), (1000, 264, 136), (4096, 1800, 200)]
+
+
+@pytest.mark.parametrize("dtype", HALF, ids=ids)
+@pytest.mark.parametrize("place", PLACES, ids=ids)
+@pytest.mark.parametrize("size", gated_sizes(), ids=ids)
+def test_gated_exact(size, place, dtype):
+    require_gpu()
+    m, inter, k = size
+    say(f"gated {size} {place} {dtype}")
+    g = generator(m + 10 * inter + 100 * k)
+    x = integers(g, m, k, dtype) * (torch.rand((m, k), generator=g, device="cuda") < min(1.0, 600 / k)).to(dtype)
+    w = integers(g, 2 * inter, k, dtype)
+    gu64 = x.double() @ w.double().T
+    h64 = act64(gu64[:, :inter], "relu")[0] * gu64[:, inter:]
+    assert float(h64.abs().max()) < 2 ** 16
+    h, gu = Output(m, inter, dtype, place[1], place[0]), Output(m, 2 * inter, dtype, place[0], place[1])
+    xp, wp = placed(x, place), placed(w, place)
+    moe.gated_linear(xp, wp, act="relu", out=h.view)
+    same(h.view, h64, "h alone")
+    h.view.fill_(5)
+    moe.gated_linear(xp, wp, act="relu", out=h.view, gu=gu.view)
+    same(h.view, h64, "h")
+    same(gu.view, gu64, "gu")
+    h.check_surroundings()
+    gu.check_surroundings()
+
+
+@pytest.mark.parametrize("dtype", HALF, ids=ids)
+@pytest.mark.parametrize("place", PLACES, ids=ids)
+@pytest.mark.parametrize("size", gated_sizes(), ids=ids)
+def test_gated_backward_exact(size, place, dtype):
+    require_gpu()
+    m, inter, k = size
+    say(f"gated backward {size} {place} {dtype}")
+    g = generator(m + 10 * inter + 100 * k + 1)
+    x, w, dh = integers(g, m, k, dtype), integers(g, 2 * inter, k, dtype), integers(g, m, inter, dtype)
+    gu = integers(g, m, 2 * inter, dtype, 3)
+    a, da = act64(gu[:, :inter].double(), "relu")
+    d = torch.cat((dh.double() * gu[:, inter:].double() * da, dh.double() * a), 1)
+    dx, dw = Output(m, k, dtype, place[1], place[0]), Output(2 * inter, k, dtype, place[0], place[1])
+    moe.gated_linear_backward(placed(dh, place), placed(x, place), placed(w, place), placed(gu, place), act="relu",
+                              dx=dx.view, dw=dw.view)
+    same(dx.view, d @ w.double(), "dx")
+    same(dw.view, d.T @ x.double(), "dw")
+    dx.check_surroundings()
+    dw.check_surroundings()
+
+
+REAL = [(1, 40, 200), (19, 72, 520), (130, 136, 264), (97, 131, 301)]
+
+
+@pytest.mark.parametrize("dtype", HALF, ids=ids)
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("size", REAL, ids=ids)
+def test_linear_activations(size, act, dtype):
+    require_gpu()
+    m, n, k = size
+    g = generator(m + n)
+    x, w = normal(g, m, k, dtype), normal(g, n, k, dtype, 3 / math.sqrt(k))
+    bias, res = normal(g, 1, n, dtype)[0], normal(g, m, n, dtype)
+    z = torch.empty((m, n), dtype=dtype, device="cuda")
+    y = moe.linear(x, w, bias=bias, act=act, residual=res, z=z)
+    z64 = x.double() @ w.double().T + bias.double()
+    ez = sum_error(k + 2, x.double().abs() @ w.double().abs().T + bias.double().abs())
+    close(z, z64, ez, "z")
+    ea = act_error(z64, ez, act)
+    want = act64(z64, act)[0] + res.double()
+    say(f"linear {size} {act} {dtype}", close(y, want, ea + F(want, ea), "y"))
+
+
+def F(value, error):
+    return 2.0 ** -24 * (value.abs() + error)
+
+
+@pytest.mark.parametrize("dtype", HALF, ids=ids)
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("size", REAL, ids=ids)
+def test_linear_backward_activations(size, act, dtype):
+    require_gpu()
+    m, n, k = size
+    g = generator(m + n + 1)
+    x, w, dy = normal(g, m, k, dtype), normal(g, n, k, dtype, 1 / math.sqrt(k)), normal(g, m, n, dtype)
+    z = normal(g, m, n, dtype, 3)
+    dx, dw, db = moe.linear_backward(dy, x, w, act=act, z=z)
+    z64, dy64 = z.double(), dy.double()
+    dz = dy64 * act64(z64, act)[1]
+    ed = dy64.abs() * grad_error(z64, act) + 2 * F(dz, 0.0)
+    er = ed if act == "none" else ed + rounding(dz.abs() + ed, dtype)
+    size_of = dz.abs() + er
+    say(f"linear backward {size} {act} {dtype}",
+        close(dx, dz @ w.double(), er @ w.double().abs() + sum_error(n, size_of @ w.double().abs()), "dx"),
+        close(dw, dz.T @ x.double(), er.T @ x.double().abs() + sum_error(m, size_of.T @ x.double().abs()), "dw"),
+        close(db, dz.sum(0), ed.sum(0) + sum_error(m, size_of.sum(0)), "dbias"))
+
+
+@pytest.mark.parametrize("dtype", HALF, ids=ids)
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("size", REAL, ids=ids)
+def test_gated_activations(size, act, dtype):
+    require_gpu()
+    m, inter, k = size
+    g = generator(m + inter + 2)
+    x, w = normal(g, m, k, dtype), normal(g, 2 * inter, k, dtype, 2 / math.sqrt(k))
+    gu = torch.empty((m, 2 * inter), dtype=dtype, device="cuda")
+    h = moe.gated_linear(x, w, act=act, gu=gu)
+    z64 = x.double() @ w.double().T
+    ez = sum_error(k, x.double().abs() @ w.double().abs().T)
+    close(gu, z64, ez, "gu")
+    gate, up, eg, eu = z64[:, :inter], z64[:, inter:], ez[:, :inter], ez[:, inter:]
+    a, ea = act64(gate, act)[0], act_error(gate, eg, act)
+    e = ea * (up.abs() + eu) + a.abs() * eu
+    say(f"gated {size} {act} {dtype}", close(h, a * up, e + F(a * up, e), "h"))
+    dh = normal(g, m, inter, dtype)
+    dx, dw = moe.gated_linear_backward(dh, x, w, gu, act=act)
+    gate, up, dh64 = gu[:, :inter].double(), gu[:, inter:].double(), dh.double()
+    a, da = act64(gate, act)
+    d = torch.cat((dh64 * up * da, dh64 * a), 1)
+    ed = torch.cat(((dh64 * up).abs() * grad_error(gate, act), dh64.abs() * act_error(gate, 0.0, act)), 1) + 3 * F(d, 0.0)
+    ed = ed + rounding(d.abs() + ed, dtype)
+    big = d.abs() + ed
+    say(f"gated backward {size} {act} {dtype}",
+        close(dx, d @ w.double(), ed @ w.double().abs() + sum_error(2 * inter, big @ w.double().abs()), "dx"),
+        close(dw, d.T @ x.double(), ed.T @ x.double().abs() + sum_error(m, big.T @ x.double().abs()), "dw"))
