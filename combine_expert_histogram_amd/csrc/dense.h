@@ -2,6 +2,9 @@
 // product, and the launches that the entry points choose from.
 #pragma once
 
+#include <type_traits>
+#include <utility>
+
 #include "common.h"
 
 namespace moe {
@@ -58,6 +61,40 @@ __device__ __forceinline__ void store8(T* p, const float (&f)[8], int n) {
     }
 }
 
+// f(0), f(1), .. f(N - 1) with constants, in line
+template <class F, int... I>
+__device__ __forceinline__ void unroll_over(F&& f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void unroll(F&& f) {
+    unroll_over(f, std::make_integer_sequence<int, N>{});
+}
+
+// ---------------------------------------------------------------- memory straight to LDS
+#define MOE_LDS(p) ((void __attribute__((address_space(3)))*)(p))
+
+// s_waitcnt immediates: at most n vector memory operations in flight; every LDS operation returned
+constexpr int wait_vm(int n) { return (n & 0xF) | (0x7 << 4) | (0xF << 8) | ((n >> 4) << 14); }
+constexpr int kWaitLds0 = 0xF | (0x7 << 4) | (0x3 << 14);
+
+// 16 bytes a lane from p + off (zeros where that is not below `bytes`) to LDS at lds + AT + 16 * lane.  In asm, since the
+// compiler takes every transposing LDS read for one that may depend on any such load in flight and waits for all of them;
+// the caller counts them (vmcnt) and waits before a barrier.  s_nop 4: the descriptor's registers may come from a
+// v_readlane, whose result a vector memory instruction may read five wait states later.  m0 is the compiler's own: it sets
+// it before each of its uses.
+template <int AT>
+__device__ __forceinline__ void load_to_lds(const void* p, int bytes, uint32_t off, uint32_t lds) {
+    const uint64_t at = (uint64_t)p;
+    const u32x4 rsrc = {(uint32_t)at, (uint32_t)(at >> 32), (uint32_t)bytes, 0x00020000u};     // addresses have 48 bits
+    asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(rsrc), "s"(lds),
+                 "i"(AT)
+                 : "memory", "scc");
+}
+
+// LDS serves a 16 B read sixteen lanes at a time: lanes 0-3, 12-15, 20-23 and 24-27, then 4-11, 16-19 and 28-31, and the
+// other half alike; the rows of two share the 256 B of its banks.
+__device__ __forceinline__ int swizzle(int r) { return r >> 1 & 7; }
 // ---------------------------------------------------------------- activations
 // In fp32; the exponential and the reciprocal are the hardware's (a few ulps), unseen behind a rounding to 16 bits.
 //   silu      z s(z), s(z) = 1 / (1 + e^-z)
@@ -139,6 +176,46 @@ __device__ __forceinline__ void activate_grad(const float (&z)[N], float (&a)[N]
     }
 }
 
+// ---------------------------------------------------------------- columns' sums, as workgroups left them
+// out_a[c] (out_b[c]) = the sum of column c (half + c) over `parts` rows of `sums`, `ld` floats (a multiple of 4) apart; each
+// may be null.  64 columns to a workgroup, four to a thread, sixteen teams that take every sixteenth row: a fixed order.
+// 512 rows of 2 x 7168: 42 us with four teams and a column to a thread.
+__host__ __device__ inline int64_t pad4(int64_t n) { return (n + 3) & ~int64_t(3); }
+
+template <class T>
+__global__ void __launch_bounds__(256) join_columns_kernel(const float* sums, int parts, int64_t ld, int half, int n, T* out_a,
+                                                           T* out_b) {
+    constexpr int kTeams = 16;
+    __shared__ f32x4 lds[kTeams][16];
+    const int lane = threadIdx.x % 16, team = threadIdx.x / 16;
+    const int64_t c = (int64_t)blockIdx.x * 64 + lane * 4;
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    if (c < ld) {
+#pragma unroll 8
+        for (int p = team; p < parts; p += kTeams) sum += *reinterpret_cast<const f32x4*>(sums + p * ld + c);
+    }
+    lds[team][lane] = sum;
+    __syncthreads();
+    if (threadIdx.x >= 64) return;
+    const int64_t at = (int64_t)blockIdx.x * 64 + threadIdx.x;
+    float s = 0.0f;
+#pragma unroll
+    for (int t = 0; t < kTeams; ++t) s += reinterpret_cast<const float*>(lds[t])[threadIdx.x];
+    if (at < n) {
+        if (out_a) out_a[at] = (T)s;
+    } else if (at >= half && at < half + n) {
+        if (out_b) out_b[at - half] = (T)s;
+    }
+}
+
+template <class T>
+inline moe_status join_columns(const float* sums, int parts, int64_t ld, int64_t half, int n, void* out_a, void* out_b,
+                               hipStream_t stream) {
+    hipLaunchKernelGGL(join_columns_kernel<T>, dim3((unsigned)((ld + 63) / 64)), dim3(256), 0, stream, sums, parts, ld, (int)half,
+                       n, static_cast<T*>(out_a), static_cast<T*>(out_b));
+    return launch_status();
+}
+
 // ---------------------------------------------------------------- the epilogue of a product
 // What becomes of the fp32 sums z[row, c]: plain ones, y = act(z + bias) + res; gated ones, y = act(g) u with g and u the
 // columns c and inter + c.  Stored once, rounded once; z (gu) as well where it is not null.
@@ -152,9 +229,15 @@ struct Epilogue {
     int act;
 };
 
-// n <= 8 columns from c of one row
+// n <= 8 columns from c of one row; res: those of the residual, read beforehand
 template <class T>
-__device__ __forceinline__ void finish(const Epilogue& e, int64_t row, int c, float (&v)[8], int n) {
+__device__ __forceinline__ typename Vec<T>::x8 residual_of(const Epilogue& e, int64_t row, int c, int n) {
+    return e.res ? load8(static_cast<const T*>(e.res) + row * e.res_ld + c, n) : typename Vec<T>::x8{};
+}
+
+template <class T>
+__device__ __forceinline__ void finish(const Epilogue& e, int64_t row, int c, float (&v)[8], int n,
+                                       const typename Vec<T>::x8& res) {
     if (e.bias) {
         const typename Vec<T>::x8 b = load8(static_cast<const T*>(e.bias) + c, n);
 #pragma unroll
@@ -163,9 +246,8 @@ __device__ __forceinline__ void finish(const Epilogue& e, int64_t row, int c, fl
     if (e.z) store8(static_cast<T*>(e.z) + row * e.z_ld + c, v, n);
     activate(v, e.act);
     if (e.res) {
-        const typename Vec<T>::x8 r = load8(static_cast<const T*>(e.res) + row * e.res_ld + c, n);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += (float)r[i];
+        for (int i = 0; i < 8; ++i) v[i] += (float)res[i];
     }
     store8(static_cast<T*>(e.y) + row * e.y_ld + c, v, n);
 }
@@ -216,6 +298,6 @@ moe_status launch_tiles_nn(int dtype, bool aligned, const Plan& plan, const Prod
                            hipStream_t stream);
 moe_status launch_tiles_tn(int dtype, bool aligned, const Plan& plan, const Product& p, const Epilogue& e, float* part,
                            hipStream_t stream);
-moe_status launch_few(int dtype, const Product& p, const Epilogue& e, hipStream_t stream);
+moe_status launch_few(int dtype, bool aligned, const Product& p, const Epilogue& e, hipStream_t stream);
 
 }  // namespace moe

@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(JoinArgs t) {
             add_parts(t, row * t.n + t.inter + c, u, n);
             finish_gated<T>(t.e, row, c, v, u, n);
         } else {
-            finish<T>(t.e, row, c, v, n);
+            finish<T>(t.e, row, c, v, n, residual_of<T>(t.e, row, c, n));
         }
     }
 }
@@ -86,7 +86,7 @@ int grid_of(int64_t items) { return (int)std::min<int64_t>((items + kThreads - 1
 moe_status run_product(Layout layout, int dtype, bool aligned, const Product& p, const Epilogue& e, void* ws,
                        hipStream_t stream) {
     const Plan plan = plan_product(layout, p.m, p.inter ? p.inter * 2 : p.n, p.k, aligned);
-    if (plan.tile == 0) return launch_few(dtype, p, e, stream);
+    if (plan.tile == 0) return launch_few(dtype, aligned, p, e, stream);
     float* part = static_cast<float*>(ws);
     moe_status st = launch_tiles(layout, dtype, aligned, plan, p, e, part, stream);
     if (st != MOE_OK || plan.splits == 1) return st;
@@ -140,7 +140,7 @@ struct DzArgs {
     const void* dy;
     const void* z;           // null: no activation
     void* d;                 // null: not kept
-    float* sums;             // [gridDim.y, n], null: not wanted
+    float* sums;             // [gridDim.y, n padded to 4], null: not wanted
     int64_t dy_ld, z_ld, d_ld, m, rows;
     int n, act;
 };
@@ -184,16 +184,7 @@ __global__ void __launch_bounds__(kThreads) dz_kernel(DzArgs t) {
     float s = 0.0f;
 #pragma unroll
     for (int g = 0; g < kRowGroups; ++g) s += lds[g][threadIdx.x];
-    t.sums[(int64_t)blockIdx.y * t.n + col] = s;
-}
-
-template <class T>
-__global__ void __launch_bounds__(kThreads) column_sum_kernel(const float* sums, int parts, int n, void* out) {
-    const int c = blockIdx.x * kThreads + threadIdx.x;
-    if (c >= n) return;
-    float s = 0.0f;
-    for (int p = 0; p < parts; ++p) s += sums[(int64_t)p * n + c];
-    static_cast<T*>(out)[c] = (T)s;
+    t.sums[(int64_t)blockIdx.y * pad4(t.n) + col] = s;
 }
 
 int64_t row_parts(int64_t m) { return std::max<int64_t>(1, std::min<int64_t>((m + 63) / 64, kMaxRowParts)); }
@@ -205,9 +196,7 @@ moe_status launch_dz(DzArgs t, void* dbias, hipStream_t stream) {
     hipLaunchKernelGGL(dz_kernel<T>, dim3((t.n + kColumns - 1) / kColumns, (int)parts), dim3(kThreads), 0, stream, t);
     moe_status st = launch_status();
     if (st != MOE_OK || !dbias) return st;
-    hipLaunchKernelGGL(column_sum_kernel<T>, dim3((t.n + kThreads - 1) / kThreads), dim3(kThreads), 0, stream, t.sums,
-                       (int)parts, t.n, dbias);
-    return launch_status();
+    return join_columns<T>(t.sums, (int)parts, pad4(t.n), pad4(t.n), t.n, dbias, nullptr, stream);
 }
 
 template <class T>
@@ -254,7 +243,7 @@ struct Backward {
 Backward backward_of(int64_t m, int64_t n, int64_t k, bool keeps) {
     Backward b;
     b.sums = keeps ? pad(m * pad8(n) * 2) : 0;
-    b.parts = b.sums + pad(row_parts(m) * n * 4);
+    b.parts = b.sums + pad(row_parts(m) * pad4(n) * 4);
     b.bytes = b.parts + std::max(product_bytes(kNN, m, k, n), product_bytes(kTN, n, k, m));
     return b;
 }

@@ -1,5 +1,18 @@
 // Tiled matrix products of 16-bit rows: C[m, n] = sum_k A(m, k) B(n, k) in fp32, each operand with K along its rows or
-// across them, a tile of BM x BN results to a workgroup.
+// across them.
+//
+// A persistent workgroup walks over tiles of BM x BN results.  Its wavefronts hold RW x CW of them each in registers
+// (v_mfma_f32_16x16x32, operands swapped, so that a lane holds four consecutive columns of a row) and take 64 of K a step
+// from a two-step ring in LDS, which loads go to directly.  All of it is one stream over the tiles: a step's last 32 of K
+// are multiplied after the barrier that frees its place, while the step after the next is loaded there and the next
+// step's first fragments are read; a tile's last steps load the next tile's first ones, which arrive while its sums are
+// written.  Two sets of fragments alternate, and the order of products, LDS reads and loads is laid out by hand.
+//
+// What bounds it (16384 x 4096 x 7168 bf16, 256 x 256 tiles, counters): the matrix cores are busy 0.67 of the time at 1.95
+// GHz, the clock that the card's power leaves them; with all operands in the caches they are busy 0.79 of it at 1.81 GHz.
+// LDS is busy a quarter of the time.  Tried: 32 x 32 MFMAs (as fast), four wavefronts of 128 x 128 (0.55 busy: one
+// wavefront a SIMD cannot multiply while its loads queue), four steps of 32 of K (as fast, slower along rows: half lines),
+// wavefront priorities (none), 128 x 128 tiles (0.8 of the rate).
 #pragma once
 
 #include "dense.h"
@@ -7,24 +20,21 @@
 namespace moe {
 namespace {
 
-#define MOE_LDS(p) ((void __attribute__((address_space(3)))*)(p))
+constexpr int kBK = kStepK;                                  // of K a step
 
-constexpr int kBK = kStepK;
-
-constexpr int wait_vm(int n) { return (n & 0xF) | (0x7 << 4) | (0xF << 8) | ((n >> 4) << 14); }
-constexpr int kWaitLds0 = 0xF | (0x7 << 4) | (0x3 << 14);
-
-template <int BM_, int BN_, int WM_, int WN_, int STAGES_>
+template <int BM_, int BN_, int WM_, int WN_>
 struct TileCfg {
-    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_;
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
     static constexpr int kWaves = WM * WN, kThreads = kWaves * MOE_WAVE;
+    static constexpr int kPerCu = 8 / kWaves;                // workgroups: two wavefronts to a SIMD
     static constexpr int RW = BM / WM, CW = BN / WN, MI = RW / 16, NJ = CW / 16;
     static constexpr int A_BYTES = BM * kBK * 2, B_BYTES = BN * kBK * 2, STAGE = A_BYTES + B_BYTES;
     static constexpr int A_LOADS = A_BYTES / 1024 / kWaves, B_LOADS = B_BYTES / 1024 / kWaves;
     static constexpr int LOADS = A_LOADS + B_LOADS;
+    static constexpr int LDS = 2 * STAGE + kWaves * 4096;    // the ring, and a piece of the epilogue's for each wavefront
     static_assert(CW == 64 && RW % 16 == 0, "the epilogue's pieces are 16 x 64");
     static_assert(A_LOADS * 1024 * kWaves == A_BYTES && B_LOADS * 1024 * kWaves == B_BYTES, "whole loads");
-    static_assert(STAGES * STAGE <= 160 * 1024 && kWaves * 4096 <= STAGES * STAGE && STAGES * LOADS < 64, "LDS");
+    static_assert(LDS * kPerCu <= 160 * 1024, "LDS");
 };
 
 struct TileArgs {
@@ -35,141 +45,167 @@ struct TileArgs {
     int kper, splits, tiles_m, tiles_n, total;
 };
 
+constexpr int kXcds = 8, kCus = 256;                         // of an MI355X
+
 enum TileEnd { kPlain, kGated, kPart };
 
-// 16 bytes a lane from p + off (zeros where that is not below `bytes`) to lds + 16 * lane.  In asm, since the compiler
-// takes every transposing LDS read for one that may depend on any such load in flight and waits for all of them; the
-// caller counts them (vmcnt) and waits before a barrier.  s_nop 4: the descriptor's registers may come from a
-// v_readlane, whose result a vector memory instruction may read five wait states later.
-__device__ __forceinline__ void load_to_lds(const void* p, int bytes, uint32_t off, uint8_t* lds) {
-    const uint64_t at = (uint64_t)p;
-    const u32x4 rsrc = {(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu, (uint32_t)bytes, 0x00020000u};
-    const uint32_t to = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)MOE_LDS(lds));
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(rsrc), "s"(to)
-                 : "memory");                // m0 is the compiler's own: it sets it before each of its uses
-}
-
-// One operand of a tile: W rows (of A or B), kBK of K a step, in LDS 1 KB pieces of which the workgroup's wavefronts load
+// One operand of a tile: W rows (of A or B), 64 of K a step, in LDS 1 KB pieces of which the workgroup's wavefronts load
 // L each.
-//   K along the rows (TR = false): row r holds 128 B, its 16 B chunk c in slot c ^ (r & 7) ^ (r >> 3 & 1), so that the
-//   sixteen rows that an MFMA operand reads at one chunk lie in sixteen different 16 B columns of the 256 B that LDS's
-//   banks span;
+//   K along the rows (TR = false): row r holds 128 B, its 16 B chunk c in slot c ^ swizzle(r), so that what LDS serves
+//   of an MFMA operand (sixteen rows, four chunks) at a time lies in different 16 B columns of the 256 B that its banks span;
 //   K across (TR = true): K step k holds 2 W bytes, the 32 B piece p (sixteen rows) in slot p ^ turn(k); read by
 //   ds_read_b64_tr_b16, in which sixteen lanes take four K steps of a piece and come out with one row's four each.
+template <int W>
+__device__ __forceinline__ int turn(int k) {
+    return ((k & 3) | (k >> 3 & 3) << 2) & (W / 16 - 1);
+}
+
 template <class T, int W, int L, bool TR, bool ALIGNED, bool PAIRED>
 struct Loader {
     typedef typename Vec<T>::x8 x8;
-    static constexpr int kChunks = W / 8;                    // TR: 16 B chunks of a K step
-    const T* base;           // TR: element (row0, k = 0); else row 0 of the operand
+    static constexpr int kChunks = TR ? W / 8 : kBK / 8;      // 16 B chunks of a row in LDS
+    static constexpr int kPer = 64 / kChunks;                // rows in LDS of a load: K steps (TR) or rows of the operand
+    const T* base;           // element (row0, k = 0) where TR; else row 0 of the operand
     int64_t ld;
     int row0, rows;          // the tile's first row; rows of the operand (PAIRED: of one half)
-    int kend;
+    int k0, kend;            // K of the next step, and its end
     int blk0, lane;
-    uint32_t off[L];
+    const T* at[ALIGNED ? L : 1];                            // load i's next place,
+    int bytes[ALIGNED ? L : 1];                              // what it may reach from there,
+    uint32_t off[ALIGNED ? L : 1];                           // and this lane's offset
     x8 held[ALIGNED ? 1 : L];
-
-    static __device__ __forceinline__ int turn(int k) { return ((k & 3) | (k >> 3 & 3) << 2) & (W / 16 - 1); }
 
     // PAIRED: every 64 rows of the tile are 32 of the gate's and the same 32 of the up projection's
     __device__ __forceinline__ int row_of(int r) const { return PAIRED ? row0 + (r >> 6) * 32 + (r & 31) : row0 + r; }
     __device__ __forceinline__ int64_t half_of(int r) const { return PAIRED && (r & 32) ? rows : 0; }
 
+    // the row in LDS and the chunk of it that lane `lane` brings with load i
+    __device__ __forceinline__ int line(int i) const { return (blk0 + i) * kPer + lane / kChunks; }
     __device__ __forceinline__ int chunk(int i) const {
-        const int b = blk0 + i;
-        if constexpr (TR) {
-            const int k = (b * 64 + lane) / kChunks;
-            return (lane % kChunks) ^ (turn(k) << 1);
-        } else {
-            return (lane & 7) ^ (lane >> 3) ^ (b & 1);
-        }
+        if constexpr (TR) return (lane % kChunks) ^ (turn<W>(line(i)) << 1);
+        else return (lane % kChunks) ^ swizzle(line(i));
     }
 
-    __device__ __forceinline__ void setup(const void* p, int64_t ld_, int row0_, int rows_, int kend_, int wave, int lane_) {
+    __device__ __forceinline__ void start(const void* p, int64_t ld_, int rows_, int wave, int lane_) {
         base = static_cast<const T*>(p);
-        ld = ld_, row0 = row0_, rows = rows_, kend = kend_, blk0 = wave * L, lane = lane_;
+        ld = ld_, rows = rows_, blk0 = wave * L, lane = lane_;
+        if constexpr (ALIGNED) {
 #pragma unroll
-        for (int i = 0; i < L; ++i) {
-            if constexpr (TR) off[i] = (uint32_t)(lane / kChunks) * (uint32_t)(ld * 2) + chunk(i) * 16;
-            else off[i] = (uint32_t)(lane >> 3) * (uint32_t)(ld * 2) + chunk(i) * 16;
+            for (int i = 0; i < L; ++i)
+                off[i] = (uint32_t)(lane / kChunks) * (uint32_t)((int)ld * 2) + chunk(i) * 16;
+        }
+    }
+    // the tile whose rows start at row0_, its K from kbeg to kend_; a tile without K gives zeros
+    __device__ __forceinline__ void tile(int row0_, int kbeg, int kend_) {
+        row0 = row0_, k0 = kbeg, kend = kend_;
+        if constexpr (ALIGNED) {
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                const int b = blk0 + i, step = (int)ld;
+                int n;                                       // elements in reach; none or a negative number: no row
+                if constexpr (TR) {
+                    at[i] = base + (int64_t)(kbeg + b * kPer) * ld + row0;
+                    n = (kPer - 1) * step + min(W, rows - row0);
+                } else {
+                    const int r = row_of(b * kPer);
+                    at[i] = base + (half_of(b * kPer) + r) * ld + kbeg;
+                    n = (min(kPer, rows - r) - 1) * step + min(kBK, kend - kbeg);
+                }
+                bytes[i] = kend > kbeg ? max(n, 0) * 2 : 0;
+            }
         }
     }
 
-    // load i of K step [k0, k0 + kBK) into its place in `lds`; what lies past the operand comes as zeros, by the range
-    // that the buffer descriptor holds
-    __device__ __forceinline__ void direct(int i, int k0, uint8_t* lds) const {
-        const int b = blk0 + i, step = (int)ld;
-        const T* p;
-        int count;               // elements in range; 0 or fewer rows leave a negative one
-        uint32_t o = off[i];
+    // load I's next piece into its place in the stage at `lds`; past the end of K come zeros
+    template <int I>
+    __device__ __forceinline__ void direct(uint32_t lds) {
+        const int k = TR ? lane / kChunks : chunk(I) * 8, left = kend - k0 - (TR ? (blk0 + I) * kPer : 0);
+        load_to_lds<I * 1024>(at[I], bytes[I], k < left ? off[I] : 0x80000000u, lds);
+        at[I] += TR ? (int64_t)kBK * ld : kBK;
+        if constexpr (I == L - 1) k0 += kBK;
+    }
+
+    // the first element of line `line` (128 bytes) of the 256 or fewer that step [k, k + 64) of the tile holds
+    __device__ __forceinline__ const T* line_at(int line, int k) const {
         if constexpr (TR) {
-            constexpr int kPer = 64 / kChunks;               // K steps of a load
-            const int k = k0 + b * kPer;
-            p = base + (int64_t)k * ld + row0;
-            count = (min(kPer, kend - k) - 1) * step + min(W, rows - row0);
+            return base + (int64_t)(k + line / (W / 64)) * ld + min(row0 + line % (W / 64) * 64, rows - 1);
         } else {
-            const int r = row_of(b * 8);
-            p = base + (half_of(b * 8) + r) * ld + k0;
-            count = (min(8, rows - r) - 1) * step + (kend - k0);
-            if (k0 + kBK > kend && k0 + chunk(i) * 8 >= kend) o = 0x80000000u;   // the last step of K, or one past it
+            const int r = min(row_of(line), rows - 1);
+            return base + (half_of(line) + r) * ld + k;
         }
-        load_to_lds(p, max(count, 0) * 2, o, lds + b * 1024);
     }
 
     // the same through registers, for rows that start anywhere: fetch, and put a step later
-    __device__ __forceinline__ void fetch(int i, int k0) {
-        const int b = blk0 + i;
+    template <int I>
+    __device__ __forceinline__ void fetch() {
         if constexpr (TR) {
-            const int k = k0 + (b * 64 + lane) / kChunks, c = row0 + chunk(i) * 8;
-            held[i] = load8(base + (int64_t)k * ld + c, k < kend ? min(8, rows - c) : 0);
+            const int k = k0 + line(I), c = row0 + chunk(I) * 8;
+            held[I] = load8(base + (int64_t)k * ld + c, k < kend ? min(8, rows - c) : 0);
         } else {
-            const int r = row_of(b * 8 + (lane >> 3)), c = k0 + chunk(i) * 8;
-            held[i] = load8(base + (half_of(b * 8) + r) * ld + c, r < rows ? min(8, kend - c) : 0);
+            const int r = row_of(line(I)), c = k0 + chunk(I) * 8;
+            held[I] = load8(base + (half_of(line(I)) + r) * ld + c, r < rows ? min(8, kend - c) : 0);
         }
+        if constexpr (I == L - 1) k0 += kBK;
     }
     __device__ __forceinline__ void put(int i, uint8_t* lds) const {
         *reinterpret_cast<x8*>(lds + (blk0 + i) * 1024 + lane * 16) = held[i];
     }
 };
 
-// A wavefront's operand of one MFMA: rows r0 .. r0 + 15 of the tile's operand, K 32 s .. + 31 of the step.
+// A wavefront's operand of one MFMA: rows r0 .. r0 + 15 of the tile's operand, K 32 s .. + 31 of the step.  `place` is the
+// lane's part of the address, which lies clear of r0's and s's bits.
+template <int W, bool TR>
+__device__ __forceinline__ uint32_t place_of(int lane) {
+    if constexpr (TR) {
+        const int k = 8 * (lane >> 4) + (lane >> 2 & 3);     // and k + 4, which turns alike
+        return k * (2 * W) + (turn<W>(k) << 5) + (lane & 3) * 8;
+    } else {
+        const int l = lane & 15;
+        return l * (2 * kBK) + (((lane >> 4) ^ swizzle(l)) << 4);
+    }
+}
+
 template <class T, int W, bool TR>
-__device__ __forceinline__ typename Vec<T>::x8 fragment(const uint8_t* lds, int r0, int s, int lane) {
+__device__ __forceinline__ typename Vec<T>::x8 fragment(const uint8_t* lds, int r0, int s, uint32_t place) {
     typedef typename Vec<T>::x8 x8;
-    const int q = lane >> 4;
     if constexpr (TR) {
         typedef short s16x4 __attribute__((ext_vector_type(4)));
         typedef __attribute__((address_space(3))) s16x4 lds_x4;
         typedef short s16x8 __attribute__((ext_vector_type(8)));
-        const int i = lane >> 2 & 3;
-        const int turn = (i | q << 2) & (W / 16 - 1);        // of K step 32 s + 8 q + 4 h + i
-        const uint8_t* p = lds + (32 * s + 8 * q + i) * (2 * W) + (((r0 >> 4) ^ turn) << 5) + (lane & 3) * 8;
+        const uint8_t* p = lds + 32 * s * (2 * W) + (place ^ (r0 << 1));
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_x4*)(p));
         const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_x4*)(p + 4 * 2 * W));
         const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
         return __builtin_bit_cast(x8, v);
     } else {
-        const int l = lane & 15;
-        const int sw = (l & 7) ^ (l >> 3);
-        return *reinterpret_cast<const x8*>(lds + (r0 + l) * 128 + (((4 * s + q) ^ sw) << 4));
+        return *reinterpret_cast<const x8*>(lds + r0 * (2 * kBK) + (place ^ (s << 6)));
     }
 }
 
-// The tile that a workgroup takes.  Workgroup b runs on XCD b % 8; each XCD takes a run of the order below, in which 8
-// row tiles go down a column before the next, so that the 32 tiles in flight on an XCD share 8 + 4 operand slabs in its
-// L2 instead of 32 + 1.
-__device__ __forceinline__ bool tile_of(const TileArgs& t, int& tm, int& tn, int& split) {
-    constexpr int kXcds = 8, kGroup = 8;
+// A workgroup's tiles.  Workgroup b runs on XCD b % 8; each XCD takes a run of the order below, in which 8 row tiles go down
+// a column before the next, so that the 32 tiles in flight on an XCD share 8 + 4 operand slabs in its L2 instead of 32 + 1.
+struct Tile {
+    int m0, n0, split, kbeg, kend, steps;
+};
+
+template <class C, bool PAIRED>
+__device__ __forceinline__ bool tile_at(const TileArgs& t, int slot, Tile& w) {
+    constexpr int kGroup = 8;
     const int per = (t.total + kXcds - 1) / kXcds;
-    const int id = (int)(blockIdx.x % kXcds) * per + (int)(blockIdx.x / kXcds);
-    if (id >= t.total) return false;
+    const int id = (int)(blockIdx.x % kXcds) * per + slot;
+    if (slot >= per || id >= t.total) return false;
     const int tiles = t.tiles_m * t.tiles_n;
-    split = id / tiles;
-    const int in = id - split * tiles;
+    w.split = id / tiles;
+    const int in = id - w.split * tiles;
     const int group = in / (kGroup * t.tiles_n);
     const int first = group * kGroup, high = min(kGroup, t.tiles_m - first);
     const int at = in - group * kGroup * t.tiles_n;
-    tm = first + at % high;
-    tn = at / high;
+    w.m0 = (first + at % high) * C::BM;
+    w.n0 = at / high * (PAIRED ? C::BN / 2 : C::BN);
+    w.kbeg = w.split * t.kper;
+    w.kend = min(t.p.k, w.kbeg + t.kper);
+    // the ring holds two
+    w.steps = max((w.kend - w.kbeg + kBK - 1) / kBK, 2);
     return true;
 }
 
@@ -178,35 +214,40 @@ __global__ void __launch_bounds__(C::kThreads, 2)
 tile_kernel(TileArgs t) {
     typedef typename Vec<T>::x8 x8;
     constexpr int MI = C::MI, NJ = C::NJ;
-    __shared__ __align__(16) uint8_t lds[C::STAGES * C::STAGE];
-    int tm, tn, split;
-    if (!tile_of(t, tm, tn, split)) return;
+    __shared__ __align__(16) uint8_t lds[C::LDS];
     const int lane = threadIdx.x % MOE_WAVE;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / MOE_WAVE);
     const int wm = wave / C::WN, wn = wave % C::WN;
-    const int m0 = tm * C::BM, n0 = tn * (PAIRED ? C::BN / 2 : C::BN);
-    const int kbeg = split * t.kper, kend = min(t.p.k, kbeg + t.kper);
-    const int steps = (kend - kbeg + kBK - 1) / kBK;
+    int slot = blockIdx.x / kXcds;
+    Tile w;
+    if (!tile_at<C, PAIRED>(t, slot, w)) return;
 
     Loader<T, C::BM, C::A_LOADS, AT, ALIGNED, false> la;
     Loader<T, C::BN, C::B_LOADS, BT, ALIGNED, PAIRED> lb;
-    la.setup(t.p.a, t.p.lda, m0, t.p.m, kend, wave, lane);
-    lb.setup(t.p.b, t.p.ldb, n0, PAIRED ? t.p.inter : t.p.n, kend, wave, lane);
+    la.start(t.p.a, t.p.lda, t.p.m, wave, lane);
+    lb.start(t.p.b, t.p.ldb, PAIRED ? t.p.inter : t.p.n, wave, lane);
+    la.tile(w.m0, w.kbeg, w.kend);
+    lb.tile(w.n0, w.kbeg, w.kend);
 
-    auto issue_a = [&](int i, int g) __attribute__((always_inline)) {
-        if constexpr (ALIGNED) la.direct(i, kbeg + g * kBK, lds + (g % C::STAGES) * C::STAGE);
-        else la.fetch(i, kbeg + g * kBK);
+    const uint32_t ring = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)MOE_LDS(lds));
+    const uint32_t ring_a = ring + wave * C::A_LOADS * 1024, ring_b = ring + C::A_BYTES + wave * C::B_LOADS * 1024;
+    // load i of the next step, A's before B's, for place `at` of the ring
+    auto issue = [&](auto i, int at) __attribute__((always_inline)) {
+        constexpr int I = decltype(i)::value;
+        if constexpr (!ALIGNED) {
+            if constexpr (I < C::A_LOADS) la.template fetch<I>();
+            else lb.template fetch<I - C::A_LOADS>();
+        } else {
+            if constexpr (I < C::A_LOADS) la.template direct<I>(ring_a + at * C::STAGE);
+            else lb.template direct<I - C::A_LOADS>(ring_b + at * C::STAGE);
+        }
     };
-    auto issue_b = [&](int i, int g) __attribute__((always_inline)) {
-        if constexpr (ALIGNED) lb.direct(i, kbeg + g * kBK, lds + (g % C::STAGES) * C::STAGE + C::A_BYTES);
-        else lb.fetch(i, kbeg + g * kBK);
-    };
-    auto put = [&](int g) __attribute__((always_inline)) {
-        uint8_t* at = lds + (g % C::STAGES) * C::STAGE;
+    auto put = [&](int at) __attribute__((always_inline)) {
+        uint8_t* to = lds + at * C::STAGE;
 #pragma unroll
-        for (int i = 0; i < C::A_LOADS; ++i) la.put(i, at);
+        for (int i = 0; i < C::A_LOADS; ++i) la.put(i, to);
 #pragma unroll
-        for (int i = 0; i < C::B_LOADS; ++i) lb.put(i, at + C::A_BYTES);
+        for (int i = 0; i < C::B_LOADS; ++i) lb.put(i, to + C::A_BYTES);
     };
     auto barrier = []() __attribute__((always_inline)) {
         asm volatile("" ::: "memory");
@@ -215,142 +256,216 @@ tile_kernel(TileArgs t) {
     };
 
     f32x4 acc[MI][NJ];
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
     x8 fa[2][MI], fb[2][NJ];
-    auto read_a = [&](int g, int s, int i) __attribute__((always_inline)) {
-        return fragment<T, C::BM, AT>(lds + (g % C::STAGES) * C::STAGE, wm * C::RW + 16 * i, s, lane);
-    };
-    auto read_b = [&](int g, int s, int j) __attribute__((always_inline)) {
-        return fragment<T, C::BN, BT>(lds + (g % C::STAGES) * C::STAGE + C::A_BYTES, wn * C::CW + 16 * j, s, lane);
-    };
-
-    // the ring: step g's loads go out as soon as every wavefront holds the last fragments of step g - STAGES, half a step
-    // before that step's MFMAs end
-    if constexpr (ALIGNED) {
-#pragma unroll
-        for (int g = 0; g < C::STAGES; ++g) {
-#pragma unroll
-            for (int i = 0; i < C::A_LOADS; ++i) issue_a(i, g);
-#pragma unroll
-            for (int i = 0; i < C::B_LOADS; ++i) issue_b(i, g);
-        }
-        __builtin_amdgcn_s_waitcnt(wait_vm((C::STAGES - 1) * C::LOADS));
-    } else {
-        static_assert(ALIGNED || C::STAGES == 2, "one step in registers, one in LDS, one free");
-#pragma unroll
-        for (int i = 0; i < C::A_LOADS; ++i) issue_a(i, 0);
-#pragma unroll
-        for (int i = 0; i < C::B_LOADS; ++i) issue_b(i, 0);
-        put(0);
-#pragma unroll
-        for (int i = 0; i < C::A_LOADS; ++i) issue_a(i, 1);
-#pragma unroll
-        for (int i = 0; i < C::B_LOADS; ++i) issue_b(i, 1);
-        __builtin_amdgcn_s_waitcnt(kWaitLds0);
-    }
-    barrier();
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) fb[0][j] = read_b(0, 0, j);
-#pragma unroll
-    for (int i = 0; i < MI; ++i) fa[0][i] = read_a(0, 0, i);
-
-    for (int g = 0; g < steps; ++g) {
-        // first half: its MFMAs, between them the reads of the second half's fragments
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            if (i < NJ) fb[1][i] = read_b(g, 1, i);
-            fa[1][i] = read_a(g, 1, i);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) acc[i][j] = mfma(fb[0][j], fa[0][i], acc[i][j]);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        if constexpr (!ALIGNED) put(g + 1);
-        // every read of step g has returned; step g + 1 has landed
-        __builtin_amdgcn_s_waitcnt(kWaitLds0);
-        if constexpr (ALIGNED) __builtin_amdgcn_s_waitcnt(wait_vm((C::STAGES - 2) * C::LOADS));
-        barrier();
-        // second half: its MFMAs, between them step g + STAGES's loads and the first reads of step g + 1
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            if (i < NJ) fb[0][i] = read_b(g + 1, 0, i);
-            fa[0][i] = read_a(g + 1, 0, i);
-#pragma unroll
-            for (int u = i * C::LOADS / MI; u < (i + 1) * C::LOADS / MI; ++u) {
-                if (u < C::A_LOADS) issue_a(u, g + C::STAGES);
-                else issue_b(u - C::A_LOADS, g + C::STAGES);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) acc[i][j] = mfma(fb[1][j], fa[1][i], acc[i][j]);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    }
-
-    // the sums through LDS, sixteen rows at a time, so that a lane holds eight columns of a row; each wavefront has 4 KB,
-    // its 16 B chunks swizzled by row
-    __builtin_amdgcn_s_waitcnt(kWaitLds0);
-    __builtin_amdgcn_s_waitcnt(wait_vm(0));
-    barrier();
-    // the wait that a read of the last MFMA's result needs; the reads below are tied behind it
-    asm volatile("s_nop 15");
-    __builtin_amdgcn_sched_barrier(0);
-    uint8_t* stage = lds + wave * 4096;
-    const int srow = lane & 15, q = lane >> 4;
-    auto staged = [&](int row, int c, float (&v)[8]) __attribute__((always_inline)) {
-        const f32x4 lo = *reinterpret_cast<const f32x4*>(stage + row * 256 + ((c ^ row) << 4));
-        const f32x4 hi = *reinterpret_cast<const f32x4*>(stage + row * 256 + (((c + 1) ^ row) << 4));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
-    };
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            asm volatile("" : "+v"(acc[i][j]));
-            *reinterpret_cast<f32x4*>(stage + srow * 256 + (((4 * j + q) ^ srow) << 4)) = acc[i][j];
-        }
-        const int mrow = m0 + wm * C::RW + 16 * i;
-        if constexpr (PAIRED && END == kGated) {
-            const int row = lane >> 2, c = (lane & 3) * 8, col = n0 + wn * 32 + c;
-            float gate[8], up[8];
-            staged(row, c / 4, gate);
-            staged(row, 8 + c / 4, up);
-            if (mrow + row < t.p.m && col < t.p.inter)
-                finish_gated<T>(t.e, mrow + row, col, gate, up, min(8, t.p.inter - col));
+    uint32_t place_a = place_of<C::BM, AT>(lane), place_b = place_of<C::BN, BT>(lane);
+    // fragment r of part s of the step in place `at`, in the order of first use: A's first, all of B's, the rest of A's
+    auto read = [&](auto r, auto set, int at, int s) __attribute__((always_inline)) {
+        constexpr int R = decltype(r)::value, S = decltype(set)::value;
+        const uint8_t* from = lds + at * C::STAGE;
+        if constexpr (R >= 1 && R <= NJ) {
+            fb[S][R - 1] = fragment<T, C::BN, BT>(from + C::A_BYTES, wn * C::CW + 16 * (R - 1), s, place_b);
         } else {
+            constexpr int i = R == 0 ? 0 : R - NJ;
+            fa[S][i] = fragment<T, C::BM, AT>(from, wm * C::RW + 16 * i, s, place_a);
+        }
+    };
+
+    // Part s of the step in place `at` (32 of K, in fragment set s): its products, and between them the reads of the next
+    // part's fragments (none after a tile's last).  Before the second part every wavefront holds its fragments and the next
+    // step has landed: from the barrier on the place is filled again.  TOUCH: requests in flight behind the step's loads.
+    constexpr int kProducts = MI * NJ, kReads = MI + NJ;
+    constexpr int kReadSpan = kProducts * 3 / 4, kLoadSpan = kProducts / 2;      // products over which they are spread
+    auto part = [&](auto s_, auto ends, auto touches, int at) __attribute__((always_inline)) {
+        constexpr int s = decltype(s_)::value;
+        constexpr bool kReadOn = !(s == 1 && decltype(ends)::value);
+        // (opaque, or the compiler keeps every fragment's address in a register through all of the kernel)
+        asm volatile("" : "+v"(place_a), "+v"(place_b));
+        if constexpr (s == 1) {
+            if constexpr (!ALIGNED) put(1 - at);
+            __builtin_amdgcn_s_waitcnt(kWaitLds0);
+            if constexpr (ALIGNED) __builtin_amdgcn_s_waitcnt(wait_vm(decltype(touches)::value));
+            barrier();
+        }
+        unroll<kProducts>([&](auto t) __attribute__((always_inline)) {
+            constexpr int i = decltype(t)::value / NJ, j = decltype(t)::value % NJ;
+            acc[i][j] = mfma(fb[s][j], fa[s][i], acc[i][j]);
+            constexpr auto due = [](int n, int all, int span) { return n * all / span < all ? n * all / span : all; };
+            constexpr int n = decltype(t)::value;
+            constexpr int r0 = kReadOn ? due(n, kReads, kReadSpan) : 0, r1 = kReadOn ? due(n + 1, kReads, kReadSpan) : 0;
+            unroll<r1 - r0>([&](auto r) __attribute__((always_inline)) {
+                read(std::integral_constant<int, r0 + decltype(r)::value>{}, std::integral_constant<int, 1 - s>{},
+                     s == 1 ? 1 - at : at, 1 - s);
+            });
+            constexpr int u0 = s == 1 ? due(n, C::LOADS, kLoadSpan) : 0, u1 = s == 1 ? due(n + 1, C::LOADS, kLoadSpan) : 0;
+            unroll<u1 - u0>([&](auto u) __attribute__((always_inline)) {
+                issue(std::integral_constant<int, u0 + decltype(u)::value>{}, at);
+            });
+            if constexpr (r1 > r0 || u1 > u0) __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+
+    // The sums through LDS, so that a lane holds eight columns of a row: pieces of 16 rows x 64 columns, one at a time (4 KB
+    // a wavefront, the 16 B chunks swizzled by row).
+    constexpr bool kPairs = PAIRED && END == kGated;
+    constexpr int kRows = kPairs ? 1 : 2;                    // of a piece to a lane
+    auto write = [&](const Tile& w) __attribute__((always_inline)) {
+        // The lane and the arguments anew: held through the loop over K they cost registers that spill, and a spilled one's
+        // reload waits for every load in flight.
+        int lane;
+        asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(lane));
+        uint64_t segment = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+        asm volatile("" : "+s"(segment));
+        const auto* from = (const __attribute__((address_space(4))) TileArgs*)segment;
+        TileArgs t;
+        t.e.bias = from->e.bias, t.e.res = from->e.res, t.e.z = from->e.z, t.e.y = from->e.y;
+        t.e.res_ld = from->e.res_ld, t.e.z_ld = from->e.z_ld, t.e.y_ld = from->e.y_ld;
+        t.e.n = from->e.n, t.e.act = from->e.act;
+        t.part = from->part, t.part_step = from->part_step;
+        t.p.m = from->p.m, t.p.n = from->p.n, t.p.inter = from->p.inter;
+        uint8_t* stage = lds + 2 * C::STAGE + wave * 4096;
+        const int lrow = kPairs ? lane >> 2 : lane >> 3, lcol = (kPairs ? lane & 3 : lane & 7) * 8;
+        // the wait that a read of the last MFMA's result needs; the reads below are tied behind it
+        asm volatile("s_nop 15");
+        __builtin_amdgcn_sched_barrier(0);
+        const int most = PAIRED ? t.p.inter : t.p.n;
+        auto staged = [&](int row, int c, float (&v)[8]) __attribute__((always_inline)) {
+            const uint8_t* at = stage + row * 256;
+            const f32x4 lo = *reinterpret_cast<const f32x4*>(at + ((c ^ row) << 4));
+            const f32x4 hi = *reinterpret_cast<const f32x4*>(at + (((c + 1) ^ row) << 4));
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int row = 8 * h + (lane >> 3), c = (lane & 7) * 8;
-                int col = n0 + wn * 64 + c, most = t.p.n;
-                if constexpr (PAIRED) {                      // gate columns, then the up projection's
-                    col = n0 + wn * 32 + (c & 31);
-                    most = t.p.inter;
+            for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
+        };
+        // the row and column that a lane finishes of a piece, and its half h
+        auto row_at = [&](int piece, int h) __attribute__((always_inline)) {
+            return w.m0 + wm * C::RW + 16 * piece + 8 * h + lrow;
+        };
+        const int col = PAIRED ? w.n0 + wn * 32 + (lcol & 31) : w.n0 + wn * 64 + lcol, n = min(8, most - col);
+        auto residual = [&](int piece, int h) __attribute__((always_inline)) {
+            const int row = row_at(piece, h);
+            return residual_of<T>(t.e, row, col, row < t.p.m ? n : 0);
+        };
+        x8 res[2][kRows];
+        if constexpr (END == kPlain) {
+#pragma unroll
+            for (int h = 0; h < kRows; ++h) res[0][h] = residual(0, h);
+        }
+#pragma unroll
+        for (int piece = 0; piece < MI; ++piece) {
+            if constexpr (END == kPlain) {
+                if (piece + 1 < MI) {
+#pragma unroll
+                    for (int h = 0; h < kRows; ++h) res[(piece + 1) & 1][h] = residual(piece + 1, h);
                 }
-                float v[8];
-                staged(row, c / 4, v);
-                if (mrow + row >= t.p.m || col >= most) continue;
-                const int n = min(8, most - col);
-                if constexpr (END == kPart) {
-                    float* at = t.part + split * t.part_step + (int64_t)(mrow + row) * t.p.n + col;
-                    if (PAIRED && (c & 32)) at += t.p.inter;
+            }
 #pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        if (x < n) at[x] = v[x];
-                } else {
-                    finish<T>(t.e, mrow + row, col, v, n);
+            for (int j = 0; j < NJ; ++j) {
+                asm volatile("" : "+v"(acc[piece][j]));
+                const int row = lane & 15;
+                *reinterpret_cast<f32x4*>(stage + row * 256 + (((4 * j + (lane >> 4)) ^ row) << 4)) = acc[piece][j];
+            }
+            if constexpr (kPairs) {
+                float gate[8], up[8];
+                staged(lrow, lcol / 4, gate);
+                staged(lrow, 8 + lcol / 4, up);
+                if (row_at(piece, 0) < t.p.m && n > 0) finish_gated<T>(t.e, row_at(piece, 0), col, gate, up, n);
+            } else {
+#pragma unroll
+                for (int h = 0; h < kRows; ++h) {
+                    const int row = row_at(piece, h);
+                    float v[8];
+                    staged(8 * h + lrow, lcol / 4, v);
+                    if (row >= t.p.m || n <= 0) continue;
+                    if constexpr (END == kPart) {
+                        float* to = t.part + w.split * t.part_step + (int64_t)row * t.p.n + col;
+                        if (PAIRED && (lcol & 32)) to += t.p.inter;      // gate columns, then the up projection's
+                        if (n == 8) {
+                            __builtin_memcpy(to, v, 32);
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < 8; ++x)
+                                if (x < n) to[x] = v[x];
+                        }
+                    } else {
+                        finish<T>(t.e, row, col, v, n, res[piece & 1][h]);
+                    }
                 }
             }
         }
+    };
+
+    // What the steps ahead will load, brought into the XCD's L2: the 32 workgroups of an XCD work side by side on 8 x 4
+    // tiles, and each asks for its share of its two operands' lines four steps early (one request a wavefront and step, 12
+    // lanes; the values go to the epilogue's corner of LDS, unread).  Where K lies along the rows of both operands, so that a
+    // step takes half a kilobyte of lines from every row: 16384 x 4096 x 7168 bf16 718 -> 676 us, gated 692 -> 662, 16384 x
+    // 7168 x 2048 with a residual 425 -> 412.  Across (dx, dw) it takes time: 692 -> 735 and 750 -> 758.
+    constexpr bool kTouch = ALIGNED && C::kPerCu == 1 && !AT && !BT;
+    constexpr std::integral_constant<int, kTouch> touches{};
+    constexpr int kAhead = 4 * kBK, kShareA = 4, kShareB = 8;
+    const uint8_t* touch_at = nullptr;
+    int64_t touch_by = 0;
+    int touch_left = 0;
+    auto touch_tile = [&]() __attribute__((always_inline)) {
+        constexpr int kLinesA = C::BM / kShareA / C::kWaves, kLinesB = C::BN / kShareB / C::kWaves;
+        const int tm = w.m0 / C::BM, tn = w.n0 / (PAIRED ? C::BN / 2 : C::BN);
+        const int k = w.kbeg + kAhead < w.kend ? w.kbeg + kAhead : w.kbeg;
+        const bool of_b = lane >= kLinesA && lane < kLinesA + kLinesB;
+        const int line = of_b ? (tm % kShareB * C::kWaves + wave) * kLinesB + lane - kLinesA
+                              : (tn % kShareA * C::kWaves + wave) * kLinesA + lane % kLinesA;
+        const uint64_t a = (uint64_t)la.line_at(line, k), b = (uint64_t)lb.line_at(line, k);
+        touch_at = reinterpret_cast<const uint8_t*>(of_b ? b : a);
+        const int64_t by_a = 2 * kBK * (AT ? t.p.lda : 1), by_b = 2 * kBK * (BT ? t.p.ldb : 1);
+        touch_by = of_b ? by_b : by_a;
+        touch_left = (w.kend - k) / kBK - 1;                 // whole steps behind that one
+    };
+    auto touch_step = [&]() __attribute__((always_inline)) {
+        asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"((uint64_t)touch_at),
+                     "s"(ring + 2 * C::STAGE + wave * 4096)
+                     : "memory");
+        touch_at += touch_left > 0 ? touch_by : 0;
+        --touch_left;
+    };
+
+    constexpr std::integral_constant<int, 0> zero{};
+    constexpr std::integral_constant<int, 1> one{};
+    unroll<C::LOADS>([&](auto i) __attribute__((always_inline)) { issue(i, 0); });
+    if constexpr (!ALIGNED) put(0);
+    unroll<C::LOADS>([&](auto i) __attribute__((always_inline)) { issue(i, 1); });
+    __builtin_amdgcn_s_waitcnt(ALIGNED ? wait_vm(C::LOADS) : kWaitLds0);
+    barrier();
+
+    // (With a workgroup to a tile, 16384 x 7168 x 2048 with a residual took 458 us instead of 430.)
+    int at = 0;
+    for (bool more = true; more;) {
+        unroll<kReads>([&](auto r) __attribute__((always_inline)) { read(r, zero, at, 0); });
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (kTouch) touch_tile();
+        for (int g = 0; g < w.steps - 2; ++g, at ^= 1) {
+            part(zero, zero, touches, at);
+            part(one, zero, touches, at);
+            if constexpr (kTouch) touch_step();
+        }
+        const Tile done = w;
+        slot += gridDim.x / kXcds;
+        more = tile_at<C, PAIRED>(t, slot, w);
+        if (!more) w.kbeg = w.kend = 0;
+        la.tile(w.m0, w.kbeg, w.kend);
+        lb.tile(w.n0, w.kbeg, w.kend);
+        part(zero, zero, zero, at);
+        part(one, zero, zero, at);
+        at ^= 1;
+        part(zero, one, zero, at);
+        part(one, one, zero, at);
+        at ^= 1;
+        write(done);
     }
+    if constexpr (ALIGNED) __builtin_amdgcn_s_waitcnt(wait_vm(0));       // the loads past the last tile
 }
 
-using Wide = TileCfg<256, 256, 2, 4, 2>;
-using Narrow = TileCfg<128, 128, 2, 2, 2>;
+using Wide = TileCfg<256, 256, 2, 4>;
+using Narrow = TileCfg<128, 128, 2, 2>;
 
 template <class T, class C, bool AT, bool BT, bool ALIGNED, TileEnd END, bool PAIRED>
 moe_status launch_tile(const Plan& plan, const Product& p, const Epilogue& e, float* part, hipStream_t stream) {
@@ -363,7 +478,7 @@ moe_status launch_tile(const Plan& plan, const Product& p, const Epilogue& e, fl
     const int64_t total = (int64_t)t.tiles_m * t.tiles_n * plan.splits;
     if (total > (1 << 24)) return MOE_ERR_UNSUPPORTED;
     t.total = (int)total;
-    hipLaunchKernelGGL((tile_kernel<T, C, AT, BT, ALIGNED, END, PAIRED>), dim3((t.total + 7) / 8 * 8),
+    hipLaunchKernelGGL((tile_kernel<T, C, AT, BT, ALIGNED, END, PAIRED>), dim3(std::min((t.total + kXcds - 1) / kXcds * kXcds, kCus * C::kPerCu)),
                        dim3(C::kThreads), 0, stream, t);
     return launch_status();
 }

@@ -29,6 +29,26 @@ __device__ __forceinline__ void loadf(const T* p, int n, float (&f)[8]) {
     }
 }
 
+// the same, kept as they lie in memory
+template <class T>
+struct Raw {
+    typename Vec<T>::x8 v;
+    __device__ __forceinline__ void load(const T* p, int n) { v = load8(p, n); }
+    __device__ __forceinline__ void floats(float (&f)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = (float)v[i];
+    }
+};
+template <>
+struct Raw<float> {
+    float v[8];
+    __device__ __forceinline__ void load(const float* p, int n) { loadf(p, n, v); }
+    __device__ __forceinline__ void floats(float (&f)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = v[i];
+    }
+};
+
 template <class T>
 __device__ __forceinline__ void storef(T* p, const float (&f)[8], int n) {
     if constexpr (sizeof(T) == 2) {
@@ -182,47 +202,72 @@ struct NormGradArgs {
     const float* mean;
     const float* rstd;
     void* dx;                // null: not wanted
-    float* sums;             // [gridDim.x, 2, cols] of dw and db, null: not wanted
+    float* sums;             // [gridDim.x, 2, cols padded to 4] of dw and db, null: not wanted
     int64_t dy_ld, x_ld, dx_ld;
     int rows, cols;
 };
 
-// A workgroup (W > 1) or a wavefront (W = 1, four to a workgroup) takes every gridDim-th row.
+// A workgroup (W > 1) or a wavefront (W = 1, four to a workgroup) takes every gridDim-th row.  16-bit rows: the next row is
+// on its way while a row is worked on, and the weights wait in LDS (asked for again with each row, they would queue behind
+// the next row's loads).
 template <class T, class P, int W, int V>
 __global__ void __launch_bounds__(W == 1 ? 256 : W * MOE_WAVE) norm_grad_kernel(NormGradArgs t) {
     constexpr int kTeam = W * MOE_WAVE, kTeams = W == 1 ? 4 : 1;
+    constexpr bool kAhead = sizeof(T) == 2;
     __shared__ float lds[2][2][W];
+    __shared__ f32x4 weight[V * kTeam][2];
     const int i = W == 1 ? threadIdx.x % MOE_WAVE : threadIdx.x;
     const int team = W == 1 ? threadIdx.x / MOE_WAVE : 0;
+    for (int k = threadIdx.x; k < V * kTeam; k += kTeam * kTeams) {
+        float w[8];
+        loadf(static_cast<const P*>(t.w) + 8 * k, t.w ? t.cols - 8 * k : 0, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) weight[k][e / 4][e % 4] = t.w ? w[e] : 1.0f;
+    }
+    __syncthreads();
     float dw[V][8], db[V][8];
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[v][e] = db[v][e] = 0.0f;
-    int turn = 0;
-    for (int64_t row = blockIdx.x * kTeams + team; row < t.rows; row += gridDim.x * kTeams, turn ^= 1) {
+    Raw<T> xr[V], dyr[V];
+    float next_mean = 0.0f, next_rstd = 0.0f;
+    auto fetch = [&](int64_t row) __attribute__((always_inline)) {
         const T* x = static_cast<const T*>(t.x) + row * t.x_ld;
         const T* dy = static_cast<const T*>(t.dy) + row * t.dy_ld;
-        const float mean = t.mean[row], rstd = t.rstd[row];
-        float f[V][8], g[V][8];
+        next_mean = t.mean[row], next_rstd = t.rstd[row];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = 8 * (kTeam * v + i);
-            loadf(x + c, t.cols - c, f[v]);
-            loadf(dy + c, t.cols - c, g[v]);
+            xr[v].load(x + c, t.cols - c);
+            dyr[v].load(dy + c, t.cols - c);
         }
+    };
+    int turn = 0;
+    const int64_t step = gridDim.x * kTeams;
+    int64_t row = blockIdx.x * kTeams + team;
+    if (kAhead && row < t.rows) fetch(row);
+    for (; row < t.rows; row += step, turn ^= 1) {
+        if (!kAhead) fetch(row);
+        const float mean = next_mean, rstd = next_rstd;
+        float f[V][8], g[V][8];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            xr[v].floats(f[v]);
+            dyr[v].floats(g[v]);
+        }
+        if (kAhead && row + step < t.rows) fetch(row + step);
         float sg = 0.0f, sgn = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = 8 * (kTeam * v + i), n = t.cols - c;
-            float w[8];
-            if (t.w) loadf(static_cast<const P*>(t.w) + c, n, w);
+            const int n = t.cols - 8 * (kTeam * v + i);
+            const f32x4 w[2] = {weight[kTeam * v + i][0], weight[kTeam * v + i][1]};
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 f[v][e] = e < n ? (f[v][e] - mean) * rstd : 0.0f;
                 dw[v][e] = fmaf(g[v][e], f[v][e], dw[v][e]);
                 db[v][e] += g[v][e];
-                if (t.w) g[v][e] *= w[e];
+                g[v][e] *= w[e / 4][e % 4];
                 sg += g[v][e];
                 sgn = fmaf(g[v][e], f[v][e], sgn);
             }
@@ -269,17 +314,17 @@ __global__ void __launch_bounds__(W == 1 ? 256 : W * MOE_WAVE) norm_grad_kernel(
             __syncthreads();
         }
         for (int c = threadIdx.x; c < t.cols; c += 256) {
-            t.sums[(int64_t)blockIdx.x * 2 * t.cols + c] = all[0][c];
-            t.sums[((int64_t)blockIdx.x * 2 + 1) * t.cols + c] = all[1][c];
+            t.sums[blockIdx.x * 2 * pad4(t.cols) + c] = all[0][c];
+            t.sums[(blockIdx.x * 2 + 1) * pad4(t.cols) + c] = all[1][c];
         }
     } else {
-        float* to = t.sums + (int64_t)blockIdx.x * 2 * t.cols;
+        float* to = t.sums + blockIdx.x * 2 * pad4(t.cols);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = 8 * (kTeam * v + i);
             if (c >= t.cols) continue;
             storef(to + c, dw[v], t.cols - c);
-            storef(to + t.cols + c, db[v], t.cols - c);
+            storef(to + pad4(t.cols) + c, db[v], t.cols - c);
         }
     }
 }
@@ -338,31 +383,9 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(NormGradArgs t) {
             db[e] += g[e];
         }
     }
-    float* to = t.sums + (int64_t)blockIdx.y * 2 * t.cols;
+    float* to = t.sums + blockIdx.y * 2 * pad4(t.cols);
     storef(to + c, dw, n);
-    storef(to + t.cols + c, db, n);
-}
-
-// dweight and dbias from the workgroups' rows of partial sums: 64 columns to a workgroup, four threads to a column, each
-// a quarter of the rows
-template <class P>
-__global__ void __launch_bounds__(256) norm_join_kernel(const float* sums, int parts, int cols, P* dweight, P* dbias) {
-    __shared__ float lds[2][4][64];
-    const int lane = threadIdx.x % 64, team = threadIdx.x / 64, c = blockIdx.x * 64 + lane;
-    const int per = (parts + 3) / 4, last = min(parts, (team + 1) * per);
-    float dw = 0.0f, db = 0.0f;
-    if (c < cols) {
-        for (int p = team * per; p < last; ++p) {
-            dw += sums[(int64_t)p * 2 * cols + c];
-            db += sums[((int64_t)p * 2 + 1) * cols + c];
-        }
-    }
-    lds[0][team][lane] = dw;
-    lds[1][team][lane] = db;
-    __syncthreads();
-    if (team != 0 || c >= cols) return;
-    if (dweight) dweight[c] = (P)((lds[0][0][lane] + lds[0][1][lane]) + (lds[0][2][lane] + lds[0][3][lane]));
-    if (dbias) dbias[c] = (P)((lds[1][0][lane] + lds[1][1][lane]) + (lds[1][2][lane] + lds[1][3][lane]));
+    storef(to + pad4(t.cols) + c, db, n);
 }
 
 // how a row is held: wavefronts to a row and pieces of eight columns to a thread; 0 pieces: read again
@@ -444,9 +467,7 @@ moe_status run_grad(const NormGradArgs& t, void* dweight, void* dbias, hipStream
             }
     }
     if (st != MOE_OK || !t.sums) return st;
-    hipLaunchKernelGGL(norm_join_kernel<P>, dim3((t.cols + 63) / 64), dim3(256), 0, stream, t.sums, grid, t.cols,
-                       static_cast<P*>(dweight), static_cast<P*>(dbias));
-    return launch_status();
+    return join_columns<P>(t.sums, grid, 2 * pad4(t.cols), pad4(t.cols), t.cols, dweight, dbias, stream);
 }
 
 template <class P>
@@ -469,7 +490,7 @@ bool bad_types(int dtype, int param_dtype) {
     return dtype < MOE_BF16 || dtype > MOE_FP32 || (param_dtype != dtype && param_dtype != MOE_FP32);
 }
 
-size_t grad_bytes(int rows, int cols) { return rows == 0 ? 0 : (size_t)grad_grid(rows, cols) * 2 * cols * sizeof(float); }
+size_t grad_bytes(int rows, int cols) { return rows == 0 ? 0 : (size_t)grad_grid(rows, cols) * 2 * pad4(cols) * sizeof(float); }
 
 }  // namespace
 }  // namespace moe
