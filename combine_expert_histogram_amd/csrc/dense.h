@@ -227,6 +227,7 @@ struct Epilogue {
     int64_t res_ld, z_ld, y_ld;
     int n;                   // columns of y
     int act;
+    int rows;                // of y
 };
 
 // n <= 8 columns from c of one row; res: those of the residual, read beforehand
@@ -275,21 +276,25 @@ struct Product {
     int64_t lda, ldb;
     int m, n, k;             // n: rows of B (gated: 2 inter)
     int inter;               // gated: columns of y, else 0
+    int b_rows;              // not 0: B (K across its rows) has this many, at most a step, for every step of A's K
 };
 
 struct Plan {
     int tile;                // 0: few rows, 128: 128 x 128 tiles, 256: 256 x 256 tiles
     int splits;              // parts of K, summed by a second launch
     int kper;                // of K to a part, a multiple of kStepK
+    bool joined;             // the sums go to a second launch
 };
 constexpr int kStepK = 64;
 
-Plan plan_product(Layout layout, int64_t m, int64_t n, int64_t k, bool aligned);
+// terms = 2: A's rows (NN) or K (TN) are two terms of one operand, kTermRows apart (see run_backward)
+Plan plan_product(Layout layout, int64_t m, int64_t n, int64_t k, bool aligned, int terms = 1);
 int64_t plan_bytes(const Plan& p, int64_t m, int64_t n);          // of fp32 partial sums
+constexpr int kTermRows = 64;
 
 bool rows_aligned(const void* p, int64_t ld, int64_t contiguous); // 16-byte rows, whole 16-byte pieces
 
-// one launch each; part: the partial sums where splits > 1
+// one launch each; part: the partial sums where the plan is joined
 moe_status launch_tiles(Layout layout, int dtype, bool aligned, const Plan& plan, const Product& p, const Epilogue& e,
                         float* part, hipStream_t stream);
 moe_status launch_tiles_nt(int dtype, bool aligned, const Plan& plan, const Product& p, const Epilogue& e, float* part,

@@ -7,10 +7,10 @@ bool rows_aligned(const void* p, int64_t ld, int64_t contiguous) {
     return ((uintptr_t)p & 15) == 0 && ld % 8 == 0 && contiguous % 8 == 0;
 }
 
-Plan plan_product(Layout layout, int64_t m, int64_t n, int64_t k, bool aligned) {
-    if (layout == kNT && m <= 64) return Plan{0, 1, (int)((k + kStepK - 1) / kStepK * kStepK)};
+Plan plan_product(Layout layout, int64_t m, int64_t n, int64_t k, bool aligned, int terms) {
+    if (layout == kNT && m <= 64) return Plan{0, 1, (int)((k + kStepK - 1) / kStepK * kStepK), false};
     const auto tiles = [&](int64_t t) { return ((m + t - 1) / t) * ((n + t - 1) / t); };
-    Plan p{128, 1, 0};
+    Plan p{128, 1, 0, false};
     int64_t slots = 512, most = tiles(128);
     if (aligned && tiles(256) >= 192) p.tile = 256, slots = 256, most = tiles(256);
     const int64_t steps = (k + kStepK - 1) / kStepK;
@@ -19,11 +19,12 @@ Plan plan_product(Layout layout, int64_t m, int64_t n, int64_t k, bool aligned) 
     const int64_t per = (steps + splits - 1) / splits;
     p.kper = (int)(per * kStepK);
     p.splits = (int)((steps + per - 1) / per);
+    p.joined = p.splits > 1 || (terms == 2 && layout == kNN);
     return p;
 }
 
 int64_t plan_bytes(const Plan& p, int64_t m, int64_t n) {
-    return p.splits > 1 ? (p.splits * m * n * 4 + 255) & ~int64_t(255) : 0;
+    return p.joined ? (p.splits * m * n * 4 + 255) & ~int64_t(255) : 0;
 }
 
 moe_status launch_tiles(Layout layout, int dtype, bool aligned, const Plan& plan, const Product& p, const Epilogue& e,
@@ -41,26 +42,31 @@ constexpr int kThreads = 256;
 struct JoinArgs {
     const float* part;
     int64_t step;            // floats of one part
+    int64_t term;            // not 0: floats from a row of the first term to its row of the second
     int64_t items;
     int splits, n, chunks, inter;
     Epilogue e;
 };
 
+__device__ __forceinline__ void add_part(const float* p, float (&v)[8], int n) {
+    if (n >= 8) {
+        float f[8];
+        __builtin_memcpy(f, p, 32);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += f[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) v[i] += p[i];
+    }
+}
+
 __device__ __forceinline__ void add_parts(const JoinArgs& t, int64_t at, float (&v)[8], int n) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 0.0f;
     for (int s = 0; s < t.splits; ++s) {
-        const float* p = t.part + s * t.step + at;
-        if (n >= 8) {
-            float f[8];
-            __builtin_memcpy(f, p, 32);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += f[i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < n) v[i] += p[i];
-        }
+        add_part(t.part + s * t.step + at, v, n);
+        if (t.term) add_part(t.part + s * t.step + t.term + at, v, n);
     }
 }
 
@@ -84,39 +90,58 @@ __global__ void __launch_bounds__(kThreads) join_kernel(JoinArgs t) {
 int grid_of(int64_t items) { return (int)std::min<int64_t>((items + kThreads - 1) / kThreads, 16384); }
 
 moe_status run_product(Layout layout, int dtype, bool aligned, const Product& p, const Epilogue& e, void* ws,
-                       hipStream_t stream) {
-    const Plan plan = plan_product(layout, p.m, p.inter ? p.inter * 2 : p.n, p.k, aligned);
+                       hipStream_t stream, int terms = 1) {
+    const Plan plan = plan_product(layout, p.m, p.n, p.k, aligned, terms);
     if (plan.tile == 0) return launch_few(dtype, aligned, p, e, stream);
     float* part = static_cast<float*>(ws);
     moe_status st = launch_tiles(layout, dtype, aligned, plan, p, e, part, stream);
-    if (st != MOE_OK || plan.splits == 1) return st;
+    if (st != MOE_OK || !plan.joined) return st;
+    const bool two = terms == 2 && layout == kNN;            // the second term's rows follow the first's
+    const int64_t rows = two ? p.m / 2 : p.m;
     JoinArgs t;
-    t.part = part, t.step = (int64_t)p.m * p.n, t.splits = plan.splits, t.n = p.n, t.inter = p.inter, t.e = e;
+    t.part = part, t.step = (int64_t)p.m * p.n, t.term = two ? rows * p.n : 0;
+    t.splits = plan.splits, t.n = p.n, t.inter = p.inter, t.e = e;
     t.chunks = (e.n + 7) / 8;
-    t.items = (int64_t)p.m * t.chunks;
+    t.items = (two ? e.rows : rows) * t.chunks;
     if (dtype == MOE_BF16) hipLaunchKernelGGL(join_kernel<__bf16>, dim3(grid_of(t.items)), dim3(kThreads), 0, stream, t);
     else hipLaunchKernelGGL(join_kernel<_Float16>, dim3(grid_of(t.items)), dim3(kThreads), 0, stream, t);
     return launch_status();
 }
 
 // ---------------------------------------------------------------- the activations' gradients
+// Up to kTermRows rows, what the products take of a gradient d is two terms, its rounding to 16 bits and the rounding of
+// what that leaves: rows 0 .. 63 and 64 .. 127 of the workspace, zeros behind the last token.  As exact as d in fp32; with
+// one term the error of a few rows' products is off by chance from that of their own rounding to twice it and more (1
+// token, 64 x 64: 1 to 2.2 times; 64 tokens and more: 1.41).  It costs little: the second term are rows that the tile has
+// anyway.  More tokens take one term, which is what their matrix instructions cost once.
+template <class T>
+__device__ __forceinline__ void store_terms(T* p, int64_t second, const float (&d)[8], int n) {
+    store8(p, d, n);
+    if (!second) return;
+    float rest[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rest[i] = d[i] - (float)(T)d[i];
+    store8(p + second, rest, n);
+}
+
 // d[row, :] = [dh u act'(g), dh act(g)]: read and written once, 8 columns of a row to a thread
 struct GateGradArgs {
     const void* dh;
     const void* gu;
     void* d;
     int64_t dh_ld, gu_ld, d_ld, items;
-    int inter, chunks, act;
+    int64_t second;          // elements to the second term, 0: one term
+    int m, inter, chunks, act;
 };
 
 template <class T>
 __global__ void __launch_bounds__(kThreads) gate_grad_kernel(GateGradArgs t) {
     for (int64_t item = (int64_t)blockIdx.x * kThreads + threadIdx.x; item < t.items; item += (int64_t)gridDim.x * kThreads) {
         const int64_t row = item / t.chunks;
-        const int c = (int)(item - row * t.chunks) * 8, n = min(8, t.inter - c);
+        const int c = (int)(item - row * t.chunks) * 8, n = min(8, t.inter - c), have = row < t.m ? n : 0;
         const T* gu = static_cast<const T*>(t.gu) + row * t.gu_ld + c;
-        const auto dh = load8(static_cast<const T*>(t.dh) + row * t.dh_ld + c, n);
-        const auto gv = load8(gu, n), uv = load8(gu + t.inter, n);
+        const auto dh = load8(static_cast<const T*>(t.dh) + row * t.dh_ld + c, have);
+        const auto gv = load8(gu, have), uv = load8(gu + t.inter, have);
         float g[8], a[8], d[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[i] = (float)gv[i];
@@ -127,8 +152,8 @@ __global__ void __launch_bounds__(kThreads) gate_grad_kernel(GateGradArgs t) {
             a[i] *= (float)dh[i];
         }
         T* to = static_cast<T*>(t.d) + row * t.d_ld + c;
-        store8(to, d, n);
-        store8(to + t.inter, a, n);
+        store_terms(to, t.second, d, n);
+        store_terms(to + t.inter, t.second, a, n);
     }
 }
 
@@ -142,6 +167,7 @@ struct DzArgs {
     void* d;                 // null: not kept
     float* sums;             // [gridDim.y, n padded to 4], null: not wanted
     int64_t dy_ld, z_ld, d_ld, m, rows;
+    int64_t second;          // elements to the second term, 0: one term
     int n, act;
 };
 
@@ -150,16 +176,17 @@ __global__ void __launch_bounds__(kThreads) dz_kernel(DzArgs t) {
     __shared__ float lds[kRowGroups][kColumns + 4];
     const int c = blockIdx.x * kColumns + (threadIdx.x % (kColumns / 8)) * 8, group = threadIdx.x / (kColumns / 8);
     const int n = min(8, t.n - c);
-    const int64_t first = blockIdx.y * t.rows, last = min(t.m, first + t.rows);
+    const int64_t first = blockIdx.y * t.rows, last = t.second ? kTermRows : min(t.m, first + t.rows);
     float sum[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
     if (n > 0) {
         for (int64_t row = first + group; row < last; row += kRowGroups) {
-            const auto dy = load8(static_cast<const T*>(t.dy) + row * t.dy_ld + c, n);
+            const int have = row < t.m ? n : 0;              // rows behind the last token: zeros
+            const auto dy = load8(static_cast<const T*>(t.dy) + row * t.dy_ld + c, have);
             float d[8];
             if (t.z) {
-                const auto zv = load8(static_cast<const T*>(t.z) + row * t.z_ld + c, n);
+                const auto zv = load8(static_cast<const T*>(t.z) + row * t.z_ld + c, have);
                 float z[8], a[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) z[i] = (float)zv[i];
@@ -170,7 +197,7 @@ __global__ void __launch_bounds__(kThreads) dz_kernel(DzArgs t) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) d[i] = (float)dy[i];
             }
-            if (t.d) store8(static_cast<T*>(t.d) + row * t.d_ld + c, d, n);
+            if (t.d) store_terms(static_cast<T*>(t.d) + row * t.d_ld + c, t.second, d, n);
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum[i] += d[i];
         }
@@ -231,37 +258,43 @@ moe_status check_sizes(int64_t m, int64_t n, int64_t k) {
     return MOE_OK;
 }
 
-int64_t product_bytes(Layout layout, int64_t m, int64_t n, int64_t k) {
-    return std::max(plan_bytes(plan_product(layout, m, n, k, true), m, n),
-                    plan_bytes(plan_product(layout, m, n, k, false), m, n));
+int64_t product_bytes(Layout layout, int64_t m, int64_t n, int64_t k, int terms = 1) {
+    return std::max(plan_bytes(plan_product(layout, m, n, k, true, terms), m, n),
+                    plan_bytes(plan_product(layout, m, n, k, false, terms), m, n));
 }
 
-// the backward passes' workspace: dz (or [dg du]), the bias's column sums, and the products' parts
+// the backward passes' workspace: dz (or [dg du]) where it is computed, in one or two terms, the bias's column sums, and
+// the products' parts
 struct Backward {
+    int terms;
     int64_t sums, parts, bytes;
 };
-Backward backward_of(int64_t m, int64_t n, int64_t k, bool keeps) {
+Backward backward_of(int64_t m, int64_t n, int64_t k, bool computed) {
     Backward b;
-    b.sums = keeps ? pad(m * pad8(n) * 2) : 0;
+    b.terms = computed && m <= kTermRows ? 2 : 1;
+    const int64_t rows = b.terms == 2 ? 2 * kTermRows : m;
+    b.sums = computed ? pad(rows * pad8(n) * 2) : 0;
     b.parts = b.sums + pad(row_parts(m) * pad4(n) * 4);
-    b.bytes = b.parts + std::max(product_bytes(kNN, m, k, n), product_bytes(kTN, n, k, m));
+    b.bytes = b.parts + std::max(product_bytes(kNN, rows, k, n, b.terms), product_bytes(kTN, n, k, rows, b.terms));
     return b;
 }
 
-// dx = d w and dw = d^T x, either of them left out where it is null
-moe_status run_backward(int64_t m, int64_t n, int64_t k, int dtype, const void* d, int64_t d_ld, const void* x, int64_t x_ld,
-                        const void* w, int64_t w_ld, void* dx, int64_t dx_ld, void* dw, int64_t dw_ld, void* ws,
-                        hipStream_t stream) {
+// dx = d w and dw = d^T x, either of them left out where it is null.  Two terms: dx's are rows of one product, summed as
+// its parts are; dw's are two steps of K, of which x's rows are read in each.
+moe_status run_backward(const Backward& b, int64_t m, int64_t n, int64_t k, int dtype, const void* d, int64_t d_ld,
+                        const void* x, int64_t x_ld, const void* w, int64_t w_ld, void* dx, int64_t dx_ld, void* dw,
+                        int64_t dw_ld, void* ws, hipStream_t stream) {
     moe_status st = MOE_OK;
+    const int rows = b.terms == 2 ? 2 * kTermRows : (int)m;
     if (dx) {
-        const Product p{d, w, d_ld, w_ld, (int)m, (int)k, (int)n, 0};
-        const Epilogue e{nullptr, nullptr, nullptr, dx, 0, 0, dx_ld, (int)k, MOE_ACT_NONE};
-        st = run_product(kNN, dtype, rows_aligned(d, d_ld, n) && rows_aligned(w, w_ld, k), p, e, ws, stream);
+        const Product p{d, w, d_ld, w_ld, rows, (int)k, (int)n, 0, 0};
+        const Epilogue e{nullptr, nullptr, nullptr, dx, 0, 0, dx_ld, (int)k, MOE_ACT_NONE, (int)m};
+        st = run_product(kNN, dtype, rows_aligned(d, d_ld, n) && rows_aligned(w, w_ld, k), p, e, ws, stream, b.terms);
     }
     if (dw && st == MOE_OK) {
-        const Product p{d, x, d_ld, x_ld, (int)n, (int)k, (int)m, 0};
-        const Epilogue e{nullptr, nullptr, nullptr, dw, 0, 0, dw_ld, (int)k, MOE_ACT_NONE};
-        st = run_product(kTN, dtype, rows_aligned(d, d_ld, n) && rows_aligned(x, x_ld, k), p, e, ws, stream);
+        const Product p{d, x, d_ld, x_ld, (int)n, (int)k, rows, 0, b.terms == 2 ? (int)m : 0};
+        const Epilogue e{nullptr, nullptr, nullptr, dw, 0, 0, dw_ld, (int)k, MOE_ACT_NONE, (int)n};
+        st = run_product(kTN, dtype, rows_aligned(d, d_ld, n) && rows_aligned(x, x_ld, k), p, e, ws, stream, b.terms);
     }
     return st;
 }
@@ -298,8 +331,8 @@ extern "C" moe_status moe_linear(int32_t m, int32_t n, int32_t k, int32_t dtype,
     const int64_t need = product_bytes(kNT, m, n, k);
     if (need && (!ws || ws_bytes < (size_t)need)) return MOE_ERR_WORKSPACE;
     if (need && misplaced(ws, 16)) return MOE_ERR_INVALID_ARG;
-    const Product p{x, w, x_stride, w_stride, m, n, k, 0};
-    const Epilogue e{bias, residual, z, y, residual_stride, z_stride, y_stride, n, act};
+    const Product p{x, w, x_stride, w_stride, m, n, k, 0, 0};
+    const Epilogue e{bias, residual, z, y, residual_stride, z_stride, y_stride, n, act, m};
     return run_product(kNT, dtype, rows_aligned(x, x_stride, k) && rows_aligned(w, w_stride, k), p, e, ws,
                        reinterpret_cast<hipStream_t>(hip_stream));
 }
@@ -343,12 +376,12 @@ extern "C" moe_status moe_linear_backward(int32_t m, int32_t n, int32_t k, int32
     if (keeps || dbias) {
         const bool kept = keeps && (dx || dw);
         const DzArgs t{dy, keeps ? z : nullptr, kept ? at : nullptr, dbias ? reinterpret_cast<float*>(at + b.sums) : nullptr,
-                       dy_stride, z_stride, pad8(n), m, 0, n, act};
+                       dy_stride, z_stride, pad8(n), m, 0, kept && b.terms == 2 ? kTermRows * pad8(n) : 0, n, act};
         st = dtype == MOE_BF16 ? launch_dz<__bf16>(t, dbias, stream) : launch_dz<_Float16>(t, dbias, stream);
         if (st != MOE_OK) return st;
         if (kept) d = at, d_ld = pad8(n);
     }
-    return run_backward(m, n, k, dtype, d, d_ld, x, x_stride, w, w_stride, dx, dx_stride, dw, dw_stride, at + b.parts, stream);
+    return run_backward(b, m, n, k, dtype, d, d_ld, x, x_stride, w, w_stride, dx, dx_stride, dw, dw_stride, at + b.parts, stream);
 }
 
 extern "C" moe_status moe_gated_linear_workspace(int32_t m, int32_t inter, int32_t hidden, size_t* bytes) {
@@ -375,8 +408,8 @@ extern "C" moe_status moe_gated_linear(int32_t m, int32_t inter, int32_t hidden,
     const int64_t need = product_bytes(kNT, m, n, hidden);
     if (need && (!ws || ws_bytes < (size_t)need)) return MOE_ERR_WORKSPACE;
     if (need && misplaced(ws, 16)) return MOE_ERR_INVALID_ARG;
-    const Product p{x, w, x_stride, w_stride, m, (int)n, hidden, inter};
-    const Epilogue e{nullptr, nullptr, gu, h, 0, gu_stride, h_stride, inter, act};
+    const Product p{x, w, x_stride, w_stride, m, (int)n, hidden, inter, 0};
+    const Epilogue e{nullptr, nullptr, gu, h, 0, gu_stride, h_stride, inter, act, m};
     return run_product(kNT, dtype, rows_aligned(x, x_stride, hidden) && rows_aligned(w, w_stride, hidden), p, e, ws,
                        reinterpret_cast<hipStream_t>(hip_stream));
 }
@@ -411,11 +444,12 @@ extern "C" moe_status moe_gated_linear_backward(int32_t m, int32_t inter, int32_
     if (!ws || ws_bytes < (size_t)b.bytes) return MOE_ERR_WORKSPACE;
     if (misplaced(ws, 16)) return MOE_ERR_INVALID_ARG;
     uint8_t* at = static_cast<uint8_t*>(ws);
-    GateGradArgs t{dh, gu, at, dh_stride, gu_stride, pad8(n), 0, inter, (inter + 7) / 8, act};
-    t.items = (int64_t)m * t.chunks;
+    const bool two = b.terms == 2;
+    GateGradArgs t{dh, gu, at, dh_stride, gu_stride, pad8(n), 0, two ? kTermRows * pad8(n) : 0, m, inter, (inter + 7) / 8, act};
+    t.items = (int64_t)(two ? kTermRows : m) * t.chunks;
     if (dtype == MOE_BF16) hipLaunchKernelGGL(gate_grad_kernel<__bf16>, dim3(grid_of(t.items)), dim3(kThreads), 0, stream, t);
     else hipLaunchKernelGGL(gate_grad_kernel<_Float16>, dim3(grid_of(t.items)), dim3(kThreads), 0, stream, t);
     if ((st = launch_status()) != MOE_OK) return st;
-    return run_backward(m, n, hidden, dtype, at, pad8(n), x, x_stride, w, w_stride, dx, dx_stride, dw, dw_stride, at + b.parts,
-                        stream);
+    return run_backward(b, m, n, hidden, dtype, at, pad8(n), x, x_stride, w, w_stride, dx, dx_stride, dw, dw_stride,
+                        at + b.parts, stream);
 }

@@ -69,6 +69,8 @@ struct Loader {
     int64_t ld;
     int row0, rows;          // the tile's first row; rows of the operand (PAIRED: of one half)
     int k0, kend;            // K of the next step, and its end
+    int kstep;               // of K from step to step
+    int64_t by;              // elements from step to step
     int blk0, lane;
     const T* at[ALIGNED ? L : 1];                            // load i's next place,
     int bytes[ALIGNED ? L : 1];                              // what it may reach from there,
@@ -86,9 +88,10 @@ struct Loader {
         else return (lane % kChunks) ^ swizzle(line(i));
     }
 
-    __device__ __forceinline__ void start(const void* p, int64_t ld_, int rows_, int wave, int lane_) {
+    __device__ __forceinline__ void start(const void* p, int64_t ld_, int rows_, bool again, int wave, int lane_) {
         base = static_cast<const T*>(p);
         ld = ld_, rows = rows_, blk0 = wave * L, lane = lane_;
+        kstep = again ? 0 : kBK, by = again ? 0 : TR ? kBK * ld : kBK;
         if constexpr (ALIGNED) {
 #pragma unroll
             for (int i = 0; i < L; ++i)
@@ -121,8 +124,8 @@ struct Loader {
     __device__ __forceinline__ void direct(uint32_t lds) {
         const int k = TR ? lane / kChunks : chunk(I) * 8, left = kend - k0 - (TR ? (blk0 + I) * kPer : 0);
         load_to_lds<I * 1024>(at[I], bytes[I], k < left ? off[I] : 0x80000000u, lds);
-        at[I] += TR ? (int64_t)kBK * ld : kBK;
-        if constexpr (I == L - 1) k0 += kBK;
+        at[I] += by;
+        if constexpr (I == L - 1) k0 += kstep;
     }
 
     // the first element of line `line` (128 bytes) of the 256 or fewer that step [k, k + 64) of the tile holds
@@ -145,7 +148,7 @@ struct Loader {
             const int r = row_of(line(I)), c = k0 + chunk(I) * 8;
             held[I] = load8(base + (half_of(line(I)) + r) * ld + c, r < rows ? min(8, kend - c) : 0);
         }
-        if constexpr (I == L - 1) k0 += kBK;
+        if constexpr (I == L - 1) k0 += kstep;
     }
     __device__ __forceinline__ void put(int i, uint8_t* lds) const {
         *reinterpret_cast<x8*>(lds + (blk0 + i) * 1024 + lane * 16) = held[i];
@@ -224,10 +227,14 @@ tile_kernel(TileArgs t) {
 
     Loader<T, C::BM, C::A_LOADS, AT, ALIGNED, false> la;
     Loader<T, C::BN, C::B_LOADS, BT, ALIGNED, PAIRED> lb;
-    la.start(t.p.a, t.p.lda, t.p.m, wave, lane);
-    lb.start(t.p.b, t.p.ldb, PAIRED ? t.p.inter : t.p.n, wave, lane);
-    la.tile(w.m0, w.kbeg, w.kend);
-    lb.tile(w.n0, w.kbeg, w.kend);
+    la.start(t.p.a, t.p.lda, t.p.m, false, wave, lane);
+    lb.start(t.p.b, t.p.ldb, PAIRED ? t.p.inter : t.p.n, BT && t.p.b_rows, wave, lane);
+    auto begin = [&](const Tile& w) __attribute__((always_inline)) {
+        la.tile(w.m0, w.kbeg, w.kend);
+        if (BT && t.p.b_rows && w.kend) lb.tile(w.n0, 0, t.p.b_rows);
+        else lb.tile(w.n0, w.kbeg, w.kend);
+    };
+    begin(w);
 
     const uint32_t ring = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)MOE_LDS(lds));
     const uint32_t ring_a = ring + wave * C::A_LOADS * 1024, ring_b = ring + C::A_BYTES + wave * C::B_LOADS * 1024;
@@ -451,8 +458,7 @@ tile_kernel(TileArgs t) {
         slot += gridDim.x / kXcds;
         more = tile_at<C, PAIRED>(t, slot, w);
         if (!more) w.kbeg = w.kend = 0;
-        la.tile(w.m0, w.kbeg, w.kend);
-        lb.tile(w.n0, w.kbeg, w.kend);
+        begin(w);
         part(zero, zero, zero, at);
         part(one, zero, zero, at);
         at ^= 1;
@@ -501,12 +507,12 @@ moe_status launch_layout(int dtype, bool aligned, const Plan& plan, const Produc
                          hipStream_t stream) {
     if constexpr (!AT && !BT) {
         if (p.inter) {
-            if (plan.splits > 1)
+            if (plan.joined)
                 return launch_end<AT, BT, kPart, true>(dtype, aligned, plan, p, e, part, stream);
             return launch_end<AT, BT, kGated, true>(dtype, aligned, plan, p, e, part, stream);
         }
     }
-    if (plan.splits > 1) return launch_end<AT, BT, kPart, false>(dtype, aligned, plan, p, e, part, stream);
+    if (plan.joined) return launch_end<AT, BT, kPart, false>(dtype, aligned, plan, p, e, part, stream);
     return launch_end<AT, BT, kPlain, false>(dtype, aligned, plan, p, e, part, stream);
 }
 
