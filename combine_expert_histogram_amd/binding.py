@@ -654,40 +654,64 @@ def _act(act: str) -> int:
     return ACTIVATIONS[act]
 
 
-def _matrix(t, name: str, rows: int, cols: int, like) -> tuple[int | None, int]:
-    """(pointer, row stride) of an optional [rows, cols] matrix of `like`'s type and device."""
+# The checks of these calls are written for few Python operations: of the 8.4 us that a norm of one row took on the host,
+# 3.6 were the C call and its launch and 4.8 the checks.
+def _first(t, name: str, dtypes) -> tuple[int, int, torch.dtype, int]:
+    """(rows, columns, type, device) of the matrix that a call's others go by."""
+    at = t.get_device()
+    if at < 0 or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {tuple(dtypes)}, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be a matrix, got {tuple(shape)}")
+    return shape[0], shape[1], t.dtype, at
+
+
+def _matrix(t, name: str, rows: int, cols: int, dtype, at: int) -> tuple[int | None, int]:
+    """(pointer, row stride) of an optional [rows, cols] matrix."""
     if t is None:
         return None, cols
-    if t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
-    return t.data_ptr(), _rows(t, name, rows, cols)
+    if t.dtype is not dtype or t.get_device() != at:
+        raise ValueError(f"{name} must be {dtype} on cuda:{at}, got {t.dtype} on {t.device}")
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] != cols:
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(shape)}")
+    step, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return t.data_ptr(), step if rows > 1 else cols
 
 
-def _vector(t, name: str, n: int, dtype, device) -> int | None:
+def _vector(t, name: str, n: int, dtype, at: int) -> int | None:
     """Pointer of an optional contiguous [n] vector."""
     if t is None:
         return None
-    if t.dtype != dtype or t.device != device or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous [{n}] vector of {dtype} on {device}, got {tuple(t.shape)} of "
+    if t.dtype is not dtype or t.get_device() != at or t.dim() != 1 or t.numel() != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous [{n}] vector of {dtype} on cuda:{at}, got {tuple(t.shape)} of "
                          f"{t.dtype} on {t.device}")
     return t.data_ptr()
 
 
-def _two_dims(t, name: str, dtypes) -> tuple[int, int]:
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be a device tensor")
-    _dtype(t, name, dtypes)
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be a matrix, got {tuple(t.shape)}")
-    return t.shape
-
-
-def _workspace(ws, device) -> tuple[int | None, int]:
+def _workspace(ws, at: int) -> tuple[int | None, int]:
     if ws is None:
         return None, 0
-    if ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"ws must be contiguous and on {device}")
+    if ws.get_device() != at or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous and on cuda:{at}")
     return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _call(at: int, fn: str, *args) -> None:
+    """As _launch, for device number `at`."""
+    call = getattr(_lib or lib(), fn)
+    if torch._C._cuda_getDevice() == at:
+        status = call(*args, torch._C._cuda_getCurrentRawStream(at))
+    else:
+        with torch.cuda.device(at):
+            status = call(*args, torch._C._cuda_getCurrentRawStream(at))
+    if status != MOE_OK:
+        raise MoeError(fn, status)
 
 
 _HALF = (torch.bfloat16, torch.float16)
@@ -719,98 +743,105 @@ def moe_gated_linear_backward_workspace(m: int, inter: int, hidden: int) -> int:
     return _bytes("moe_gated_linear_backward_workspace", m, inter, hidden)
 
 
-def _param_dtype(x, weight, bias):
-    p = next((t.dtype for t in (weight, bias) if t is not None), x.dtype)
-    if p not in (x.dtype, torch.float32):
-        raise ValueError(f"parameters must be {x.dtype} or float32, got {p}")
-    return p
+def _param_dtype(dtype, *params):
+    for t in params:
+        if t is not None:
+            if t.dtype is not dtype and t.dtype is not torch.float32:
+                raise ValueError(f"parameters must be {dtype} or float32, got {t.dtype}")
+            return t.dtype
+    return dtype
 
 
 def moe_layer_norm(x, weight, bias, eps: float, y, mean, rstd) -> None:
-    rows, cols = _two_dims(x, "x", tuple(DTYPES))
-    p, dev = _param_dtype(x, weight, bias), x.device
-    xs = _rows(x, "x", rows, cols)
-    yp, ys = _matrix(y, "y", rows, cols, x)
-    _launch(dev, "moe_layer_norm", rows, cols, DTYPES[x.dtype], DTYPES[p], x.data_ptr(), xs,
-            _vector(weight, "weight", cols, p, dev), _vector(bias, "bias", cols, p, dev), float(eps), yp, ys,
-            _vector(mean, "mean", rows, torch.float32, dev), _vector(rstd, "rstd", rows, torch.float32, dev))
+    rows, cols, dtype, at = _first(x, "x", DTYPES)
+    p = _param_dtype(dtype, weight, bias)
+    xp, xs = _matrix(x, "x", rows, cols, dtype, at)
+    yp, ys = _matrix(y, "y", rows, cols, dtype, at)
+    _call(at, "moe_layer_norm", rows, cols, DTYPES[dtype], DTYPES[p], xp, xs, _vector(weight, "weight", cols, p, at),
+          _vector(bias, "bias", cols, p, at), eps, yp, ys, _vector(mean, "mean", rows, torch.float32, at),
+          _vector(rstd, "rstd", rows, torch.float32, at))
 
 
 def moe_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, ws) -> None:
-    rows, cols = _two_dims(x, "x", tuple(DTYPES))
-    p, dev = _param_dtype(x, weight if weight is not None else dweight, dbias), x.device
-    xs = _rows(x, "x", rows, cols)
-    dyp, dys = _matrix(dy, "dy", rows, cols, x)
-    dxp, dxs = _matrix(dx, "dx", rows, cols, x)
-    wp, wb = _workspace(ws, dev)
-    _launch(dev, "moe_layer_norm_backward", rows, cols, DTYPES[x.dtype], DTYPES[p], dyp, dys, x.data_ptr(), xs,
-            _vector(weight, "weight", cols, p, dev), _vector(mean, "mean", rows, torch.float32, dev),
-            _vector(rstd, "rstd", rows, torch.float32, dev), dxp, dxs, _vector(dweight, "dweight", cols, p, dev),
-            _vector(dbias, "dbias", cols, p, dev), wp, wb)
+    rows, cols, dtype, at = _first(x, "x", DTYPES)
+    p = _param_dtype(dtype, weight, dweight, dbias)
+    xp, xs = _matrix(x, "x", rows, cols, dtype, at)
+    dyp, dys = _matrix(dy, "dy", rows, cols, dtype, at)
+    dxp, dxs = _matrix(dx, "dx", rows, cols, dtype, at)
+    sp, sb = _workspace(ws, at)
+    _call(at, "moe_layer_norm_backward", rows, cols, DTYPES[dtype], DTYPES[p], dyp, dys, xp, xs,
+          _vector(weight, "weight", cols, p, at), _vector(mean, "mean", rows, torch.float32, at),
+          _vector(rstd, "rstd", rows, torch.float32, at), dxp, dxs, _vector(dweight, "dweight", cols, p, at),
+          _vector(dbias, "dbias", cols, p, at), sp, sb)
 
 
 def moe_linear(x, w, bias, act: str, residual, z, y, ws) -> None:
-    m, k = _two_dims(x, "x", _HALF)
-    n = _two_dims(w, "w", _HALF)[0]
-    xs = _rows(x, "x", m, k)
-    wp, wst = _matrix(w, "w", n, k, x)
-    rp, rs = _matrix(residual, "residual", m, n, x)
-    zp, zs = _matrix(z, "z", m, n, x)
-    yp, ys = _matrix(y, "y", m, n, x)
-    sp, sb = _workspace(ws, x.device)
-    _launch(x.device, "moe_linear", m, n, k, DTYPES[x.dtype], x.data_ptr(), xs, wp, wst,
-            _vector(bias, "bias", n, x.dtype, x.device), _act(act), rp, rs, zp, zs, yp, ys, sp, sb)
+    m, k, dtype, at = _first(x, "x", _HALF)
+    n = w.shape[0]
+    xp, xs = _matrix(x, "x", m, k, dtype, at)
+    wp, wst = _matrix(w, "w", n, k, dtype, at)
+    rp, rs = _matrix(residual, "residual", m, n, dtype, at)
+    zp, zs = _matrix(z, "z", m, n, dtype, at)
+    yp, ys = _matrix(y, "y", m, n, dtype, at)
+    sp, sb = _workspace(ws, at)
+    _call(at, "moe_linear", m, n, k, DTYPES[dtype], xp, xs, wp, wst, _vector(bias, "bias", n, dtype, at), _act(act), rp, rs,
+          zp, zs, yp, ys, sp, sb)
+
+
+def _columns(*matrices) -> int:
+    """Columns of the first matrix that there is."""
+    for t in matrices:
+        if t is not None:
+            return t.shape[-1]
+    return 1
 
 
 def moe_linear_backward(dy, x, w, act: str, z, dx, dw, dbias, ws) -> None:
-    """x may be None without dw, w without dx; then their sizes are the outputs'."""
-    m, n = _two_dims(dy, "dy", _HALF)
-    of = next((t for t in (x, w, dx, dw) if t is not None), None)
-    k = 1 if of is None else _two_dims(of, "x, w, dx or dw", _HALF)[1]
-    dys = _rows(dy, "dy", m, n)
-    xp, xs = _matrix(x, "x", m, k, dy)
-    wp, wst = _matrix(w, "w", n, k, dy)
-    zp, zs = _matrix(z, "z", m, n, dy)
-    dxp, dxs = _matrix(dx, "dx", m, k, dy)
-    dwp, dws = _matrix(dw, "dw", n, k, dy)
-    sp, sb = _workspace(ws, dy.device)
-    _launch(dy.device, "moe_linear_backward", m, n, k, DTYPES[dy.dtype], dy.data_ptr(), dys, xp, xs, wp, wst, _act(act),
-            zp, zs, dxp, dxs, dwp, dws, _vector(dbias, "dbias", n, dy.dtype, dy.device), sp, sb)
+    """x may be None without dw, w without dx."""
+    m, n, dtype, at = _first(dy, "dy", _HALF)
+    k = _columns(x, w, dx, dw)
+    dyp, dys = _matrix(dy, "dy", m, n, dtype, at)
+    xp, xs = _matrix(x, "x", m, k, dtype, at)
+    wp, wst = _matrix(w, "w", n, k, dtype, at)
+    zp, zs = _matrix(z, "z", m, n, dtype, at)
+    dxp, dxs = _matrix(dx, "dx", m, k, dtype, at)
+    dwp, dws = _matrix(dw, "dw", n, k, dtype, at)
+    sp, sb = _workspace(ws, at)
+    _call(at, "moe_linear_backward", m, n, k, DTYPES[dtype], dyp, dys, xp, xs, wp, wst, _act(act), zp, zs, dxp, dxs, dwp,
+          dws, _vector(dbias, "dbias", n, dtype, at), sp, sb)
 
 
 def _inter(w) -> int:
-    n = _two_dims(w, "w", _HALF)[0]
+    n = w.shape[0]
     if n < 2 or n % 2:
         raise ValueError(f"w must hold the gate's rows and as many of the up projection's, got {n}")
     return n // 2
 
 
 def moe_gated_linear(x, w, act: str, gu, h, ws) -> None:
-    m, k = _two_dims(x, "x", _HALF)
+    m, k, dtype, at = _first(x, "x", _HALF)
     inter = _inter(w)
-    xs = _rows(x, "x", m, k)
-    wp, wst = _matrix(w, "w", 2 * inter, k, x)
-    gp, gs = _matrix(gu, "gu", m, 2 * inter, x)
-    hp, hs = _matrix(h, "h", m, inter, x)
-    sp, sb = _workspace(ws, x.device)
-    _launch(x.device, "moe_gated_linear", m, inter, k, DTYPES[x.dtype], x.data_ptr(), xs, wp, wst, _act(act), gp, gs, hp,
-            hs, sp, sb)
+    xp, xs = _matrix(x, "x", m, k, dtype, at)
+    wp, wst = _matrix(w, "w", 2 * inter, k, dtype, at)
+    gp, gs = _matrix(gu, "gu", m, 2 * inter, dtype, at)
+    hp, hs = _matrix(h, "h", m, inter, dtype, at)
+    sp, sb = _workspace(ws, at)
+    _call(at, "moe_gated_linear", m, inter, k, DTYPES[dtype], xp, xs, wp, wst, _act(act), gp, gs, hp, hs, sp, sb)
 
 
 def moe_gated_linear_backward(dh, x, w, gu, act: str, dx, dw, ws) -> None:
     """x may be None without dw, w without dx."""
-    m, inter = _two_dims(dh, "dh", _HALF)
-    of = next((t for t in (x, w, dx, dw) if t is not None), None)
-    k = 1 if of is None else _two_dims(of, "x, w, dx or dw", _HALF)[1]
-    dhs = _rows(dh, "dh", m, inter)
-    gp, gs = _matrix(gu, "gu", m, 2 * inter, dh)
-    xp, xs = _matrix(x, "x", m, k, dh)
-    wp, wst = _matrix(w, "w", 2 * inter, k, dh)
-    dxp, dxs = _matrix(dx, "dx", m, k, dh)
-    dwp, dws = _matrix(dw, "dw", 2 * inter, k, dh)
-    sp, sb = _workspace(ws, dh.device)
-    _launch(dh.device, "moe_gated_linear_backward", m, inter, k, DTYPES[dh.dtype], dh.data_ptr(), dhs, gp, gs, xp, xs, wp,
-            wst, _act(act), dxp, dxs, dwp, dws, sp, sb)
+    m, inter, dtype, at = _first(dh, "dh", _HALF)
+    k = _columns(x, w, dx, dw)
+    dhp, dhs = _matrix(dh, "dh", m, inter, dtype, at)
+    gp, gs = _matrix(gu, "gu", m, 2 * inter, dtype, at)
+    xp, xs = _matrix(x, "x", m, k, dtype, at)
+    wp, wst = _matrix(w, "w", 2 * inter, k, dtype, at)
+    dxp, dxs = _matrix(dx, "dx", m, k, dtype, at)
+    dwp, dws = _matrix(dw, "dw", 2 * inter, k, dtype, at)
+    sp, sb = _workspace(ws, at)
+    _call(at, "moe_gated_linear_backward", m, inter, k, DTYPES[dtype], dhp, dhs, gp, gs, xp, xs, wp, wst, _act(act), dxp,
+          dxs, dwp, dws, sp, sb)
 
 
 def _alloc_bytes(n: int, device) -> torch.Tensor:
@@ -884,7 +915,7 @@ def linear_backward(dy, x, w, act: str = "none", z=None, bias: bool = True, dx=N
 def gated_linear(x, w, act: str = "silu", gu=None, out=None, ws=None):
     """act(x wg^T) * (x wu^T): x [m, hidden], w [2*inter, hidden] (the gate's rows, then the up projection's; bfloat16 or
     float16) -> [m, inter].  gu [m, 2*inter] is filled with both projections where given: gated_linear_backward reads it."""
-    m, k, inter = x.shape[0], x.shape[-1], w.shape[0] // 2
+    m, k, inter = x.shape[0], x.shape[-1], _inter(w)
     out = torch.empty((m, inter), dtype=x.dtype, device=x.device) if out is None else out
     if ws is None and moe_gated_linear_workspace(m, inter, k):
         ws = alloc_gated_linear_workspace(m, inter, k, x.device)

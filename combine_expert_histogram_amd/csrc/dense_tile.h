@@ -48,6 +48,8 @@ struct TileArgs {
 constexpr int kXcds = 8, kCus = 256;                         // of an MI355X
 
 enum TileEnd { kPlain, kGated, kPart };
+// the operands' rows: whole 16-byte pieces on 16-byte boundaries; anywhere, eight elements and more; anything
+enum Rows { kAligned, kAnywhere, kTiny };
 
 // One operand of a tile: W rows (of A or B), 64 of K a step, in LDS 1 KB pieces of which the workgroup's wavefronts load
 // L each.
@@ -60,8 +62,9 @@ __device__ __forceinline__ int turn(int k) {
     return ((k & 3) | (k >> 3 & 3) << 2) & (W / 16 - 1);
 }
 
-template <class T, int W, int L, bool TR, bool ALIGNED, bool PAIRED>
+template <class T, int W, int L, bool TR, Rows ROWS, bool PAIRED>
 struct Loader {
+    static constexpr bool ALIGNED = ROWS == kAligned;
     typedef typename Vec<T>::x8 x8;
     static constexpr int kChunks = TR ? W / 8 : kBK / 8;      // 16 B chunks of a row in LDS
     static constexpr int kPer = 64 / kChunks;                // rows in LDS of a load: K steps (TR) or rows of the operand
@@ -76,6 +79,7 @@ struct Loader {
     int bytes[ALIGNED ? L : 1];                              // what it may reach from there,
     uint32_t off[ALIGNED ? L : 1];                           // and this lane's offset
     x8 held[ALIGNED ? 1 : L];
+    int held_k0, held_kend, held_row0;
 
     // PAIRED: every 64 rows of the tile are 32 of the gate's and the same 32 of the up projection's
     __device__ __forceinline__ int row_of(int r) const { return PAIRED ? row0 + (r >> 6) * 32 + (r & 31) : row0 + r; }
@@ -138,20 +142,47 @@ struct Loader {
         }
     }
 
-    // the same through registers, for rows that start anywhere: fetch, and put a step later
+    // The same through registers: fetch, and put a step later.  kAnywhere takes whole 16-byte pieces, which memory serves
+    // from any address: a row past the end is the last one again, and a piece that runs over its row's end is fetched from
+    // eight elements before the end and shifted to its place, zeros behind it, where it is put.
     template <int I>
     __device__ __forceinline__ void fetch() {
+        const int l = line(I), c = chunk(I) * 8;
         if constexpr (TR) {
-            const int k = k0 + line(I), c = row0 + chunk(I) * 8;
-            held[I] = load8(base + (int64_t)k * ld + c, k < kend ? min(8, rows - c) : 0);
+            const int k = k0 + l;
+            if constexpr (ROWS == kTiny)
+                held[I] = load8(base + (int64_t)k * ld + row0 + c, k < kend ? min(8, rows - row0 - c) : 0);
+            else
+                __builtin_memcpy(&held[I], base + (int64_t)max(min(k, kend - 1), 0) * ld + min(row0 + c, rows - 8), 16);
         } else {
-            const int r = row_of(line(I)), c = k0 + chunk(I) * 8;
-            held[I] = load8(base + (half_of(line(I)) + r) * ld + c, r < rows ? min(8, kend - c) : 0);
+            const int r = row_of(l);
+            if constexpr (ROWS == kTiny)
+                held[I] = load8(base + (half_of(l) + r) * ld + k0 + c, r < rows ? min(8, kend - k0 - c) : 0);
+            else
+                __builtin_memcpy(&held[I], base + (half_of(l) + min(r, rows - 1)) * ld + max(min(k0 + c, kend - 8), 0), 16);
         }
+        if constexpr (I == 0) held_k0 = k0, held_kend = kend, held_row0 = row0;
         if constexpr (I == L - 1) k0 += kstep;
     }
-    __device__ __forceinline__ void put(int i, uint8_t* lds) const {
-        *reinterpret_cast<x8*>(lds + (blk0 + i) * 1024 + lane * 16) = held[i];
+    __device__ __forceinline__ void put(uint8_t* lds) const {
+        const bool whole = held_k0 + kBK <= held_kend && (!TR || held_row0 + W <= rows);
+        if (ROWS == kTiny || whole) {
+#pragma unroll
+            for (int i = 0; i < L; ++i) *reinterpret_cast<x8*>(lds + (blk0 + i) * 1024 + lane * 16) = held[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                const int c = chunk(i) * 8, over = TR ? held_row0 + c - (rows - 8) : held_k0 + c - (held_kend - 8);
+                const bool in = !TR || held_k0 + line(i) < held_kend;
+                const int by = 16 * max(over, 0);
+                typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+                const u64x2 v = __builtin_bit_cast(u64x2, held[i]);
+                u64x2 o = {by < 64 ? v.x >> by | (by ? v.y << (64 - by) : 0) : by < 128 ? v.y >> (by - 64) : 0,
+                           by < 64 ? v.y >> by : 0};
+                if (!in) o = u64x2{0, 0};
+                *reinterpret_cast<u64x2*>(lds + (blk0 + i) * 1024 + lane * 16) = o;
+            }
+        }
     }
 };
 
@@ -212,11 +243,12 @@ __device__ __forceinline__ bool tile_at(const TileArgs& t, int slot, Tile& w) {
     return true;
 }
 
-template <class T, class C, bool AT, bool BT, bool ALIGNED, TileEnd END, bool PAIRED>
+template <class T, class C, bool AT, bool BT, Rows ROWS, TileEnd END, bool PAIRED>
 __global__ void __launch_bounds__(C::kThreads, 2)
 tile_kernel(TileArgs t) {
     typedef typename Vec<T>::x8 x8;
     constexpr int MI = C::MI, NJ = C::NJ;
+    constexpr bool ALIGNED = ROWS == kAligned;
     __shared__ __align__(16) uint8_t lds[C::LDS];
     const int lane = threadIdx.x % MOE_WAVE;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / MOE_WAVE);
@@ -225,8 +257,8 @@ tile_kernel(TileArgs t) {
     Tile w;
     if (!tile_at<C, PAIRED>(t, slot, w)) return;
 
-    Loader<T, C::BM, C::A_LOADS, AT, ALIGNED, false> la;
-    Loader<T, C::BN, C::B_LOADS, BT, ALIGNED, PAIRED> lb;
+    Loader<T, C::BM, C::A_LOADS, AT, ROWS, false> la;
+    Loader<T, C::BN, C::B_LOADS, BT, ROWS, PAIRED> lb;
     la.start(t.p.a, t.p.lda, t.p.m, false, wave, lane);
     lb.start(t.p.b, t.p.ldb, PAIRED ? t.p.inter : t.p.n, BT && t.p.b_rows, wave, lane);
     auto begin = [&](const Tile& w) __attribute__((always_inline)) {
@@ -251,10 +283,8 @@ tile_kernel(TileArgs t) {
     };
     auto put = [&](int at) __attribute__((always_inline)) {
         uint8_t* to = lds + at * C::STAGE;
-#pragma unroll
-        for (int i = 0; i < C::A_LOADS; ++i) la.put(i, to);
-#pragma unroll
-        for (int i = 0; i < C::B_LOADS; ++i) lb.put(i, to + C::A_BYTES);
+        la.put(to);
+        lb.put(to + C::A_BYTES);
     };
     auto barrier = []() __attribute__((always_inline)) {
         asm volatile("" ::: "memory");
@@ -473,7 +503,7 @@ tile_kernel(TileArgs t) {
 using Wide = TileCfg<256, 256, 2, 4>;
 using Narrow = TileCfg<128, 128, 2, 2>;
 
-template <class T, class C, bool AT, bool BT, bool ALIGNED, TileEnd END, bool PAIRED>
+template <class T, class C, bool AT, bool BT, Rows ROWS, TileEnd END, bool PAIRED>
 moe_status launch_tile(const Plan& plan, const Product& p, const Epilogue& e, float* part, hipStream_t stream) {
     TileArgs t;
     t.p = p, t.e = e, t.part = part, t.part_step = (int64_t)p.m * p.n;
@@ -482,24 +512,29 @@ moe_status launch_tile(const Plan& plan, const Product& p, const Epilogue& e, fl
     const int columns = PAIRED ? p.inter : p.n, width = PAIRED ? C::BN / 2 : C::BN;
     t.tiles_n = (columns + width - 1) / width;
     const int64_t total = (int64_t)t.tiles_m * t.tiles_n * plan.splits;
-    if (total > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+    if (total >= (1 << 30)) return MOE_ERR_UNSUPPORTED;
     t.total = (int)total;
-    hipLaunchKernelGGL((tile_kernel<T, C, AT, BT, ALIGNED, END, PAIRED>), dim3(std::min((t.total + kXcds - 1) / kXcds * kXcds, kCus * C::kPerCu)),
+    hipLaunchKernelGGL((tile_kernel<T, C, AT, BT, ROWS, END, PAIRED>), dim3(std::min((t.total + kXcds - 1) / kXcds * kXcds, kCus * C::kPerCu)),
                        dim3(C::kThreads), 0, stream, t);
     return launch_status();
+}
+
+template <class T, bool AT, bool BT, TileEnd END, bool PAIRED>
+moe_status launch_rows(bool aligned, const Plan& plan, const Product& p, const Epilogue& e, float* part, hipStream_t stream) {
+    if (aligned) {
+        if (plan.tile == 256) return launch_tile<T, Wide, AT, BT, kAligned, END, PAIRED>(plan, p, e, part, stream);
+        return launch_tile<T, Narrow, AT, BT, kAligned, END, PAIRED>(plan, p, e, part, stream);
+    }
+    if (std::min(AT ? p.m : p.k, BT ? p.n : p.k) < 8)
+        return launch_tile<T, Narrow, AT, BT, kTiny, END, PAIRED>(plan, p, e, part, stream);
+    return launch_tile<T, Narrow, AT, BT, kAnywhere, END, PAIRED>(plan, p, e, part, stream);
 }
 
 template <bool AT, bool BT, TileEnd END, bool PAIRED>
 moe_status launch_end(int dtype, bool aligned, const Plan& plan, const Product& p, const Epilogue& e, float* part,
                       hipStream_t stream) {
-    if (dtype == MOE_BF16) {
-        if (!aligned) return launch_tile<__bf16, Narrow, AT, BT, false, END, PAIRED>(plan, p, e, part, stream);
-        if (plan.tile == 256) return launch_tile<__bf16, Wide, AT, BT, true, END, PAIRED>(plan, p, e, part, stream);
-        return launch_tile<__bf16, Narrow, AT, BT, true, END, PAIRED>(plan, p, e, part, stream);
-    }
-    if (!aligned) return launch_tile<_Float16, Narrow, AT, BT, false, END, PAIRED>(plan, p, e, part, stream);
-    if (plan.tile == 256) return launch_tile<_Float16, Wide, AT, BT, true, END, PAIRED>(plan, p, e, part, stream);
-    return launch_tile<_Float16, Narrow, AT, BT, true, END, PAIRED>(plan, p, e, part, stream);
+    if (dtype == MOE_BF16) return launch_rows<__bf16, AT, BT, END, PAIRED>(aligned, plan, p, e, part, stream);
+    return launch_rows<_Float16, AT, BT, END, PAIRED>(aligned, plan, p, e, part, stream);
 }
 
 template <bool AT, bool BT>

@@ -110,47 +110,48 @@ __global__ void __launch_bounds__(W == 1 ? 256 : W * MOE_WAVE) norm_kernel(NormA
     constexpr int kTeam = W * MOE_WAVE, kTeams = W == 1 ? 4 : 1;
     __shared__ float lds[2][W];
     const int i = W == 1 ? threadIdx.x % MOE_WAVE : threadIdx.x;
-    const int row = blockIdx.x * kTeams + (W == 1 ? threadIdx.x / MOE_WAVE : 0);
-    if (row >= t.rows) return;                               // whole wavefronts, where no barrier follows
-    const T* x = static_cast<const T*>(t.x) + row * t.x_ld;
-    float f[V][8];
-    float sum = 0.0f;
+    const int64_t step = (int64_t)gridDim.x * kTeams;
+    for (int64_t row = (int64_t)blockIdx.x * kTeams + (W == 1 ? threadIdx.x / MOE_WAVE : 0); row < t.rows; row += step) {
+        const T* x = static_cast<const T*>(t.x) + row * t.x_ld;
+        float f[V][8];
+        float sum = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int c = 8 * (kTeam * v + i);
-        loadf(x + c, t.cols - c, f[v]);
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum += f[v][e];
-    const float mean = row_sum<W>(sum, lds[0]) / (float)t.cols;
-    float sq = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int n = t.cols - 8 * (kTeam * v + i);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            f[v][e] = e < n ? f[v][e] - mean : 0.0f;
-            sq = fmaf(f[v][e], f[v][e], sq);
+        for (int v = 0; v < V; ++v) {
+            const int c = 8 * (kTeam * v + i);
+            loadf(x + c, t.cols - c, f[v]);
         }
-    }
-    const float rstd = 1.0f / sqrtf(row_sum<W>(sq, lds[1]) / (float)t.cols + t.eps);
-    T* y = static_cast<T*>(t.y) + row * t.y_ld;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int c = 8 * (kTeam * v + i), n = t.cols - c;
-        if (n <= 0) continue;
-        float w[8], b[8];
-        if (t.w) loadf(static_cast<const P*>(t.w) + c, n, w);
-        if (t.b) loadf(static_cast<const P*>(t.b) + c, n, b);
+        for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[v][e] = fmaf(f[v][e] * rstd, t.w ? w[e] : 1.0f, t.b ? b[e] : 0.0f);
-        storef(y + c, f[v], n);
-    }
-    if (i == 0) {
-        if (t.mean) t.mean[row] = mean;
-        if (t.rstd) t.rstd[row] = rstd;
+            for (int e = 0; e < 8; ++e) sum += f[v][e];
+        const float mean = row_sum<W>(sum, lds[0]) / (float)t.cols;
+        float sq = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int n = t.cols - 8 * (kTeam * v + i);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                f[v][e] = e < n ? f[v][e] - mean : 0.0f;
+                sq = fmaf(f[v][e], f[v][e], sq);
+            }
+        }
+        const float rstd = 1.0f / sqrtf(row_sum<W>(sq, lds[1]) / (float)t.cols + t.eps);
+        T* y = static_cast<T*>(t.y) + row * t.y_ld;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = 8 * (kTeam * v + i), n = t.cols - c;
+            if (n <= 0) continue;
+            float w[8], b[8];
+            if (t.w) loadf(static_cast<const P*>(t.w) + c, n, w);
+            if (t.b) loadf(static_cast<const P*>(t.b) + c, n, b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[v][e] = fmaf(f[v][e] * rstd, t.w ? w[e] : 1.0f, t.b ? b[e] : 0.0f);
+            storef(y + c, f[v], n);
+        }
+        if (i == 0) {
+            if (t.mean) t.mean[row] = mean;
+            if (t.rstd) t.rstd[row] = rstd;
+        }
     }
 }
 
@@ -158,40 +159,41 @@ __global__ void __launch_bounds__(W == 1 ? 256 : W * MOE_WAVE) norm_kernel(NormA
 template <class T, class P>
 __global__ void __launch_bounds__(1024) norm_long_kernel(NormArgs t) {
     __shared__ float lds[2][16];
-    const int64_t row = blockIdx.x;
-    const T* x = static_cast<const T*>(t.x) + row * t.x_ld;
-    float sum = 0.0f, f[8];
-    for (int c = 8 * threadIdx.x; c < t.cols; c += 8192) {
-        loadf(x + c, t.cols - c, f);
+    for (int64_t row = blockIdx.x; row < t.rows; row += gridDim.x) {
+        const T* x = static_cast<const T*>(t.x) + row * t.x_ld;
+        float sum = 0.0f, f[8];
+        for (int c = 8 * threadIdx.x; c < t.cols; c += 8192) {
+            loadf(x + c, t.cols - c, f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum += f[e];
-    }
-    const float mean = row_sum<16>(sum, lds[0]) / (float)t.cols;
-    float sq = 0.0f;
-    for (int c = 8 * threadIdx.x; c < t.cols; c += 8192) {
-        const int n = t.cols - c;
-        loadf(x + c, n, f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float d = e < n ? f[e] - mean : 0.0f;
-            sq = fmaf(d, d, sq);
+            for (int e = 0; e < 8; ++e) sum += f[e];
         }
-    }
-    const float rstd = 1.0f / sqrtf(row_sum<16>(sq, lds[1]) / (float)t.cols + t.eps);
-    T* y = static_cast<T*>(t.y) + row * t.y_ld;
-    for (int c = 8 * threadIdx.x; c < t.cols; c += 8192) {
-        const int n = t.cols - c;
-        float w[8], b[8];
-        loadf(x + c, n, f);
-        if (t.w) loadf(static_cast<const P*>(t.w) + c, n, w);
-        if (t.b) loadf(static_cast<const P*>(t.b) + c, n, b);
+        const float mean = row_sum<16>(sum, lds[0]) / (float)t.cols;
+        float sq = 0.0f;
+        for (int c = 8 * threadIdx.x; c < t.cols; c += 8192) {
+            const int n = t.cols - c;
+            loadf(x + c, n, f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = fmaf((f[e] - mean) * rstd, t.w ? w[e] : 1.0f, t.b ? b[e] : 0.0f);
-        storef(y + c, f, n);
-    }
-    if (threadIdx.x == 0) {
-        if (t.mean) t.mean[row] = mean;
-        if (t.rstd) t.rstd[row] = rstd;
+            for (int e = 0; e < 8; ++e) {
+                const float d = e < n ? f[e] - mean : 0.0f;
+                sq = fmaf(d, d, sq);
+            }
+        }
+        const float rstd = 1.0f / sqrtf(row_sum<16>(sq, lds[1]) / (float)t.cols + t.eps);
+        T* y = static_cast<T*>(t.y) + row * t.y_ld;
+        for (int c = 8 * threadIdx.x; c < t.cols; c += 8192) {
+            const int n = t.cols - c;
+            float w[8], b[8];
+            loadf(x + c, n, f);
+            if (t.w) loadf(static_cast<const P*>(t.w) + c, n, w);
+            if (t.b) loadf(static_cast<const P*>(t.b) + c, n, b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = fmaf((f[e] - mean) * rstd, t.w ? w[e] : 1.0f, t.b ? b[e] : 0.0f);
+            storef(y + c, f, n);
+        }
+        if (threadIdx.x == 0) {
+            if (t.mean) t.mean[row] = mean;
+            if (t.rstd) t.rstd[row] = rstd;
+        }
     }
 }
 
@@ -333,35 +335,36 @@ __global__ void __launch_bounds__(W == 1 ? 256 : W * MOE_WAVE) norm_grad_kernel(
 template <class T, class P>
 __global__ void __launch_bounds__(1024) norm_grad_long_kernel(NormGradArgs t) {
     __shared__ float lds[2][16];
-    const int64_t row = blockIdx.x;
-    const T* x = static_cast<const T*>(t.x) + row * t.x_ld;
-    const T* dy = static_cast<const T*>(t.dy) + row * t.dy_ld;
-    const float mean = t.mean[row], rstd = t.rstd[row];
-    float f[8], g[8], w[8], sg = 0.0f, sgn = 0.0f;
-    auto load = [&](int c) __attribute__((always_inline)) {
-        const int n = t.cols - c;
-        loadf(x + c, n, f);
-        loadf(dy + c, n, g);
-        if (t.w) loadf(static_cast<const P*>(t.w) + c, n, w);
+    for (int64_t row = blockIdx.x; row < t.rows; row += gridDim.x) {
+        const T* x = static_cast<const T*>(t.x) + row * t.x_ld;
+        const T* dy = static_cast<const T*>(t.dy) + row * t.dy_ld;
+        const float mean = t.mean[row], rstd = t.rstd[row];
+        float f[8], g[8], w[8], sg = 0.0f, sgn = 0.0f;
+        auto load = [&](int c) __attribute__((always_inline)) {
+            const int n = t.cols - c;
+            loadf(x + c, n, f);
+            loadf(dy + c, n, g);
+            if (t.w) loadf(static_cast<const P*>(t.w) + c, n, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            f[e] = e < n ? (f[e] - mean) * rstd : 0.0f;
-            if (t.w) g[e] *= w[e];
+            for (int e = 0; e < 8; ++e) {
+                f[e] = e < n ? (f[e] - mean) * rstd : 0.0f;
+                if (t.w) g[e] *= w[e];
+            }
+        };
+        for (int c = 8 * threadIdx.x; c < t.cols; c += 8192) {
+            load(c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sg += g[e], sgn = fmaf(g[e], f[e], sgn);
         }
-    };
-    for (int c = 8 * threadIdx.x; c < t.cols; c += 8192) {
-        load(c);
+        sg = row_sum<16>(sg, lds[0]) / (float)t.cols;
+        sgn = row_sum<16>(sgn, lds[1]) / (float)t.cols;
+        T* dx = static_cast<T*>(t.dx) + row * t.dx_ld;
+        for (int c = 8 * threadIdx.x; c < t.cols; c += 8192) {
+            load(c);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sg += g[e], sgn = fmaf(g[e], f[e], sgn);
-    }
-    sg = row_sum<16>(sg, lds[0]) / (float)t.cols;
-    sgn = row_sum<16>(sgn, lds[1]) / (float)t.cols;
-    T* dx = static_cast<T*>(t.dx) + row * t.dx_ld;
-    for (int c = 8 * threadIdx.x; c < t.cols; c += 8192) {
-        load(c);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = rstd * (g[e] - sg - f[e] * sgn);
-        storef(dx + c, g, t.cols - c);
+            for (int e = 0; e < 8; ++e) g[e] = rstd * (g[e] - sg - f[e] * sgn);
+            storef(dx + c, g, t.cols - c);
+        }
     }
 }
 
@@ -392,7 +395,7 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(NormGradArgs t) {
 struct Hold {
     int waves, pieces;
 };
-constexpr int kMaxLong = 1024;                               // rows of partial sums
+constexpr int kMostGroups = 1 << 20;                         // of a launch, which holds less than 2^32 threads
 
 Hold hold_of(int cols) {
     if (cols <= 2048) return Hold{1, (cols + 511) / 512};
@@ -412,7 +415,8 @@ int grad_grid(int rows, int cols) {
 template <class T, class P, int W, int V>
 moe_status launch_norm(const NormArgs& t, hipStream_t stream) {
     const int rows = W == 1 ? 4 : 1, threads = W == 1 ? 256 : W * MOE_WAVE;
-    hipLaunchKernelGGL((norm_kernel<T, P, W, V>), dim3((t.rows + rows - 1) / rows), dim3(threads), 0, stream, t);
+    hipLaunchKernelGGL((norm_kernel<T, P, W, V>), dim3(std::min((t.rows + rows - 1) / rows, kMostGroups)), dim3(threads), 0,
+                       stream, t);
     return launch_status();
 }
 
@@ -436,7 +440,7 @@ moe_status run_norm(const NormArgs& t, hipStream_t stream) {
         case 36: return launch_norm<T, P, 4, 4>(t, stream);
         case 68: return launch_norm<T, P, 8, 4>(t, stream);
         default:
-            hipLaunchKernelGGL((norm_long_kernel<T, P>), dim3(t.rows), dim3(1024), 0, stream, t);
+            hipLaunchKernelGGL((norm_long_kernel<T, P>), dim3(std::min(t.rows, kMostGroups)), dim3(1024), 0, stream, t);
             return launch_status();
     }
 }
@@ -462,7 +466,7 @@ moe_status run_grad(const NormGradArgs& t, void* dweight, void* dbias, hipStream
                 st = launch_status();
             }
             if (t.dx && st == MOE_OK) {
-                hipLaunchKernelGGL((norm_grad_long_kernel<T, P>), dim3(t.rows), dim3(1024), 0, stream, t);
+                hipLaunchKernelGGL((norm_grad_long_kernel<T, P>), dim3(std::min(t.rows, kMostGroups)), dim3(1024), 0, stream, t);
                 st = launch_status();
             }
     }

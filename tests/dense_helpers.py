@@ -128,8 +128,133 @@ def linear_sizes():
     return [(1, 1, 1), (1, 16, 8), (1, 7168, 2048), (2, 33, 65), (15, 24, 136), (16, 128, 128), (17, 100, 1000),
             (33, 17, 127), (48, 64, 320), (49, 8, 64), (64, 264, 520), (65, 8, 8), (65, 130, 72), (100, 1, 37),
             (127, 129, 63), (128, 128, 64), (129, 128, 65), (200, 392, 1160), (256, 256, 2048), (70, 96, 8200),
-            (300, 1031, 257), (1000, 520, 136), (4096, 3400, 200)]
+            (300, 1031, 257), (1000, 520, 136), (4096, 3400, 200), (130, 5, 200), (131, 200, 5), (67, 9, 11), (300, 259, 333)]
 
 
 def ids(v):
     return "x".join(str(i) for i in v) if isinstance(v, tuple) else str(v).replace("torch.", "")
+
+
+def held(value, m, dtype):
+    """What the products' 16-bit operand leaves of a gradient of this size: a rounding, or with up to 64 tokens, where a
+    second term holds that, its rounding"""
+    once = rounding(value, dtype)
+    return rounding(once, dtype) if m <= 64 else once
+
+
+def F(value, error=0.0):
+    """One rounding to fp32 of a value within `error` of this one"""
+    return F32_HALF * (value.abs() + error)
+
+
+def check_linear(x, w, bias, act, res, z, y):
+    k = x.shape[1]
+    x64, w64 = x.double(), w.double()
+    b64 = torch.zeros(w.shape[0], dtype=torch.float64, device=x.device) if bias is None else bias.double()
+    z64 = x64 @ w64.T + b64
+    ez = sum_error(k + 2, x64.abs() @ w64.abs().T + b64.abs())
+    if z is not None:
+        close(z, z64, ez, "z")
+    ea = act_error(z64, ez, act)
+    want = act64(z64, act)[0]
+    if res is not None:
+        want = want + res.double()
+        ea = ea + F(want, ea)
+    return close(y, want, ea, "y")
+
+
+def check_linear_backward(dy, x, w, act, z, dx, dw, db):
+    m, n = dy.shape
+    dy64 = dy.double()
+    if act == "none":
+        dz, ed = dy64, torch.zeros_like(dy64)
+        er = ed
+    else:
+        z64 = z.double()
+        dz = dy64 * act64(z64, act)[1]
+        ed = dy64.abs() * grad_error(z64, act) + 2 * F(dz)
+        er = ed + held(dz.abs() + ed, m, dy.dtype)
+    size, worst = dz.abs() + er, []
+    if dx is not None:
+        w64 = w.double()
+        worst.append(close(dx, dz @ w64, er @ w64.abs() + sum_error(2 * n, size @ w64.abs()), "dx"))
+    if dw is not None:
+        x64 = x.double()
+        worst.append(close(dw, dz.T @ x64, er.T @ x64.abs() + sum_error(2 * m, size.T @ x64.abs()), "dw"))
+    if db is not None:
+        worst.append(close(db, dz.sum(0), ed.sum(0) + sum_error(m, size.sum(0)), "dbias"))
+    return worst
+
+
+def check_gated(x, w, act, gu, h):
+    inter, k = h.shape[1], x.shape[1]
+    x64, w64 = x.double(), w.double()
+    z64, ez = x64 @ w64.T, sum_error(k, x64.abs() @ w64.abs().T)
+    if gu is not None:
+        close(gu, z64, ez, "gu")
+    gate, up, eg, eu = z64[:, :inter], z64[:, inter:], ez[:, :inter], ez[:, inter:]
+    a, ea = act64(gate, act)[0], act_error(gate, eg, act)
+    e = ea * (up.abs() + eu) + a.abs() * eu
+    return close(h, a * up, e + F(a * up, e), "h")
+
+
+def check_gated_backward(dh, x, w, gu, act, dx, dw):
+    m, inter = dh.shape
+    gate, up, dh64 = gu[:, :inter].double(), gu[:, inter:].double(), dh.double()
+    a, da = act64(gate, act)
+    d = torch.cat((dh64 * up * da, dh64 * a), 1)
+    ed = torch.cat(((dh64 * up).abs() * grad_error(gate, act), dh64.abs() * act_error(gate, 0.0, act)), 1) + 3 * F(d)
+    ed = ed + held(d.abs() + ed, m, dh.dtype)
+    size, worst = d.abs() + ed, []
+    if dx is not None:
+        w64 = w.double()
+        worst.append(close(dx, d @ w64, ed @ w64.abs() + sum_error(4 * inter, size @ w64.abs()), "dx"))
+    if dw is not None:
+        x64 = x.double()
+        worst.append(close(dw, d.T @ x64, ed.T @ x64.abs() + sum_error(2 * m, size.T @ x64.abs()), "dw"))
+    return worst
+
+
+def check_norm(x, w, b, eps, y, mean, rstd, what):
+    """mean: a sum of H terms.  c = x - mean carries the mean's error and a rounding; the variance 2 |c| ec from each
+    square and the sum's roundings; rstd half the variance's relative error, a division, a root and a sum; y three more."""
+    H = x.shape[1]
+    x64 = x.double()
+    w64 = torch.ones(H, dtype=torch.float64, device=x.device) if w is None else w.double()
+    b64 = torch.zeros(H, dtype=torch.float64, device=x.device) if b is None else b.double()
+    m = x64.sum(1, keepdim=True) / H
+    em = F32_HALF * (H + 4) * x64.abs().sum(1, keepdim=True) / H
+    c = x64 - m
+    ec = em + F32_HALF * (c.abs() + em)
+    v = (c * c).sum(1, keepdim=True) / H
+    ev = ((2 * c.abs() * ec + ec * ec).sum(1, keepdim=True) + F32_HALF * (H + 4) * ((c.abs() + ec) ** 2).sum(1, keepdim=True)) / H
+    r = 1 / torch.sqrt(v + eps)
+    rel = ev / (v + eps)
+    assert float(rel.max()) < 0.5
+    er = r * (rel + 4 * F32_HALF)                                   # 1/sqrt(1 - t) - 1 <= t for t < 0.5
+    want = c * r * w64 + b64
+    ey = (ec * (r + er) + c.abs() * er) * w64.abs() + 3 * F32_HALF * ((c * r * w64).abs() + b64.abs())
+    worst = close(y, want, ey, what + " y")
+    if mean is not None:
+        close(mean, m[:, 0], em[:, 0] + F32_HALF * m[:, 0].abs(), what + " mean")
+        close(rstd, r[:, 0], er[:, 0], what + " rstd")
+    return worst
+
+
+def check_norm_backward(dy, x, w, mean, rstd, dx, dweight, dbias, what):
+    """n = (x - mean) rstd takes two roundings and g = dy w one; the rows' and columns' sums a rounding a term."""
+    rows, H = x.shape
+    w64 = torch.ones(H, dtype=torch.float64, device=x.device) if w is None else w.double()
+    m, r, dy64 = mean.double()[:, None], rstd.double()[:, None], dy.double()
+    n, g = (x.double() - m) * r, dy64 * w64
+    sg, sgn = g.sum(1, keepdim=True) / H, (g * n).sum(1, keepdim=True) / H
+    e1 = F32_HALF * (H + 5) * g.abs().sum(1, keepdim=True) / H
+    e2 = F32_HALF * (H + 9) * (g * n).abs().sum(1, keepdim=True) / H
+    if dx is not None:
+        size = g.abs() + sg.abs() + (n * sgn).abs()
+        e = r * (e1 + n.abs() * e2 * (1 + 3 * F32_HALF) + 9 * F32_HALF * size)
+        close(dx, r * (g - sg - n * sgn), e, what + " dx")
+    if dweight is not None:
+        close(dweight, (dy64 * n).sum(0), F32_HALF * (rows + 10) * (dy64 * n).abs().sum(0), what + " dweight")
+    if dbias is not None:
+        close(dbias, dy64.sum(0), F32_HALF * (rows + 4) * dy64.abs().sum(0), what + " dbias")

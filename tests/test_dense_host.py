@@ -124,6 +124,9 @@ def test_workspaces(L):
     assert b.moe_linear_workspace(1, 7168, 2048) == 0 and b.moe_linear_workspace(64, 4096, 7168) == 0
     assert b.moe_linear_workspace(16384, 7168, 2048) == 0 and b.moe_linear_workspace(0, 8, 8) == 0
     assert b.moe_gated_linear_workspace(16384, 2048, 7168) == 0
+    for fn in (b.moe_linear_workspace, b.moe_gated_linear_workspace, b.moe_gated_linear_backward_workspace):
+        assert fn(0, 8, 8) >= 0
+    assert b.moe_linear_backward_workspace(0, 8, 8, "none") >= 0 and b.moe_linear_backward_workspace(0, 8, 8, "gelu") >= 0
     for m, n, k in ((65, 8, 8200), (300, 200, 4096), (1000, 777, 1111)):
         assert b.moe_linear_workspace(m, n, k) % 256 == 0
     # dz of two bytes an element, rows padded to eight, and something for the sums

@@ -6,8 +6,8 @@ import pytest
 import torch
 
 import combine_expert_histogram_amd as moe
-from dense_helpers import (ACTS, HALF, Output, act64, act_error, close, generator, grad_error, ids, inside, integers,
-                           linear_sizes, normal, rounding, same, sum_error)
+from dense_helpers import (ACTS, HALF, Output, act64, check_gated, check_gated_backward, check_linear, check_linear_backward,
+                           generator, ids, inside, integers, linear_sizes, normal, same)
 from gpu_helpers import require_gpu, say
 
 pytestmark = pytest.mark.gpu
@@ -131,23 +131,7 @@ def test_linear_activations(size, act, dtype):
     bias, res = normal(g, 1, n, dtype)[0], normal(g, m, n, dtype)
     z = torch.empty((m, n), dtype=dtype, device="cuda")
     y = moe.linear(x, w, bias=bias, act=act, residual=res, z=z)
-    z64 = x.double() @ w.double().T + bias.double()
-    ez = sum_error(k + 2, x.double().abs() @ w.double().abs().T + bias.double().abs())
-    close(z, z64, ez, "z")
-    ea = act_error(z64, ez, act)
-    want = act64(z64, act)[0] + res.double()
-    say(f"linear {size} {act} {dtype}", close(y, want, ea + F(want, ea), "y"))
-
-
-def held(value, m, dtype):
-    """What the products' 16-bit operand leaves of a gradient of this size: a rounding, or with up to 64 tokens, where a
-    second term holds that, its rounding"""
-    once = rounding(value, dtype)
-    return rounding(once, dtype) if m <= 64 else once
-
-
-def F(value, error):
-    return 2.0 ** -24 * (value.abs() + error)
+    say(f"linear {size} {act} {dtype}", check_linear(x, w, bias, act, res, z, y))
 
 
 @pytest.mark.parametrize("dtype", HALF, ids=ids)
@@ -159,16 +143,8 @@ def test_linear_backward_activations(size, act, dtype):
     g = generator(m + n + 1)
     x, w, dy = normal(g, m, k, dtype), normal(g, n, k, dtype, 1 / math.sqrt(k)), normal(g, m, n, dtype)
     z = normal(g, m, n, dtype, 3)
-    dx, dw, db = moe.linear_backward(dy, x, w, act=act, z=z)
-    z64, dy64 = z.double(), dy.double()
-    dz = dy64 * act64(z64, act)[1]
-    ed = dy64.abs() * grad_error(z64, act) + 2 * F(dz, 0.0)
-    er = ed if act == "none" else ed + held(dz.abs() + ed, m, dtype)
-    size_of = dz.abs() + er
-    say(f"linear backward {size} {act} {dtype}",
-        close(dx, dz @ w.double(), er @ w.double().abs() + sum_error(n, size_of @ w.double().abs()), "dx"),
-        close(dw, dz.T @ x.double(), er.T @ x.double().abs() + sum_error(m, size_of.T @ x.double().abs()), "dw"),
-        close(db, dz.sum(0), ed.sum(0) + sum_error(m, size_of.sum(0)), "dbias"))
+    got = moe.linear_backward(dy, x, w, act=act, z=z)
+    say(f"linear backward {size} {act} {dtype}", check_linear_backward(dy, x, w, act, z, *got))
 
 
 @pytest.mark.parametrize("dtype", HALF, ids=ids)
@@ -181,21 +157,7 @@ def test_gated_activations(size, act, dtype):
     x, w = normal(g, m, k, dtype), normal(g, 2 * inter, k, dtype, 2 / math.sqrt(k))
     gu = torch.empty((m, 2 * inter), dtype=dtype, device="cuda")
     h = moe.gated_linear(x, w, act=act, gu=gu)
-    z64 = x.double() @ w.double().T
-    ez = sum_error(k, x.double().abs() @ w.double().abs().T)
-    close(gu, z64, ez, "gu")
-    gate, up, eg, eu = z64[:, :inter], z64[:, inter:], ez[:, :inter], ez[:, inter:]
-    a, ea = act64(gate, act)[0], act_error(gate, eg, act)
-    e = ea * (up.abs() + eu) + a.abs() * eu
-    say(f"gated {size} {act} {dtype}", close(h, a * up, e + F(a * up, e), "h"))
+    say(f"gated {size} {act} {dtype}", check_gated(x, w, act, gu, h))
     dh = normal(g, m, inter, dtype)
-    dx, dw = moe.gated_linear_backward(dh, x, w, gu, act=act)
-    gate, up, dh64 = gu[:, :inter].double(), gu[:, inter:].double(), dh.double()
-    a, da = act64(gate, act)
-    d = torch.cat((dh64 * up * da, dh64 * a), 1)
-    ed = torch.cat(((dh64 * up).abs() * grad_error(gate, act), dh64.abs() * act_error(gate, 0.0, act)), 1) + 3 * F(d, 0.0)
-    ed = ed + held(d.abs() + ed, m, dtype)
-    big = d.abs() + ed
     say(f"gated backward {size} {act} {dtype}",
-        close(dx, d @ w.double(), ed @ w.double().abs() + sum_error(2 * inter, big @ w.double().abs()), "dx"),
-        close(dw, d.T @ x.double(), ed.T @ x.double().abs() + sum_error(m, big.T @ x.double().abs()), "dw"))
+        check_gated_backward(dh, x, w, gu, act, *moe.gated_linear_backward(dh, x, w, gu, act=act)))

@@ -6,7 +6,7 @@ import torch
 
 import combine_expert_histogram_amd as moe
 from dense_helpers import F32_HALF as F
-from dense_helpers import Output, close, generator, ids, inside, normal
+from dense_helpers import (Output, check_norm, check_norm_backward, generator, ids, inside, normal)
 from gpu_helpers import require_gpu, say
 
 pytestmark = pytest.mark.gpu
@@ -32,32 +32,6 @@ def parameters(g, cols, p):
     return (1 + 0.2 * torch.randn(cols, generator=g, device="cuda")).to(p), torch.randn(cols, generator=g, device="cuda").to(p)
 
 
-def check_forward(x, w, b, eps, y, mean, rstd, what):
-    """mean: a sum of H terms.  c = x - mean carries the mean's error and a rounding; the variance 2 |c| ec from each
-    square and the sum's roundings; rstd half the variance's relative error, a division, a root and a sum; y three more."""
-    H = x.shape[1]
-    x64 = x.double()
-    w64 = torch.ones(H, dtype=torch.float64, device=x.device) if w is None else w.double()
-    b64 = torch.zeros(H, dtype=torch.float64, device=x.device) if b is None else b.double()
-    m = x64.sum(1, keepdim=True) / H
-    em = F * (H + 4) * x64.abs().sum(1, keepdim=True) / H
-    c = x64 - m
-    ec = em + F * (c.abs() + em)
-    v = (c * c).sum(1, keepdim=True) / H
-    ev = ((2 * c.abs() * ec + ec * ec).sum(1, keepdim=True) + F * (H + 4) * ((c.abs() + ec) ** 2).sum(1, keepdim=True)) / H
-    r = 1 / torch.sqrt(v + eps)
-    rel = ev / (v + eps)
-    assert float(rel.max()) < 0.5
-    er = r * (rel + 4 * F)                                   # 1/sqrt(1 - t) - 1 <= t for t < 0.5
-    want = c * r * w64 + b64
-    ey = (ec * (r + er) + c.abs() * er) * w64.abs() + 3 * F * ((c * r * w64).abs() + b64.abs())
-    worst = close(y, want, ey, what + " y")
-    if mean is not None:
-        close(mean, m[:, 0], em[:, 0] + F * m[:, 0].abs(), what + " mean")
-        close(rstd, r[:, 0], er[:, 0], what + " rstd")
-    return worst
-
-
 @pytest.mark.parametrize("types", TYPES, ids=lambda t: ids(t))
 @pytest.mark.parametrize("size", SIZES, ids=ids)
 def test_forward(size, types):
@@ -70,38 +44,19 @@ def test_forward(size, types):
     mean = torch.full((rows,), math.nan, device="cuda")
     rstd = torch.full((rows,), math.nan, device="cuda")
     y = moe.layer_norm(x, w, b, eps=EPS, mean=mean, rstd=rstd)
-    worst = check_forward(x, w, b, EPS, y, mean, rstd, str(size))
+    worst = check_norm(x, w, b, EPS, y, mean, rstd, str(size))
     say(f"norm {size} {types}: {worst:.3f} of the bound")
     for lead, pad in ((0, 3), (1, 0), (8, 8)):
         out = Output(rows, cols, T, pad, lead)
         moe.layer_norm(inside(x, pad, lead), w, b, eps=EPS, out=out.view)
         assert torch.equal(out.view, y)
         out.check_surroundings()
-    check_forward(x, None, None, EPS, moe.layer_norm(x, eps=EPS), None, None, "no parameters")
-    check_forward(x, w, None, 0.5, moe.layer_norm(x, w, eps=0.5), None, None, "no bias")
-    check_forward(x, None, b, EPS, moe.layer_norm(x, None, b, eps=EPS), None, None, "no weight")
+    check_norm(x, None, None, EPS, moe.layer_norm(x, eps=EPS), None, None, "no parameters")
+    check_norm(x, w, None, 0.5, moe.layer_norm(x, w, eps=0.5), None, None, "no bias")
+    check_norm(x, None, b, EPS, moe.layer_norm(x, None, b, eps=EPS), None, None, "no weight")
     same = x.clone()
     moe.layer_norm(same, w, b, eps=EPS, out=same)
     assert torch.equal(same, y), "in place"
-
-
-def check_backward(dy, x, w, mean, rstd, dx, dweight, dbias, what):
-    """n = (x - mean) rstd takes two roundings and g = dy w one; the rows' and columns' sums a rounding a term."""
-    rows, H = x.shape
-    w64 = torch.ones(H, dtype=torch.float64, device=x.device) if w is None else w.double()
-    m, r, dy64 = mean.double()[:, None], rstd.double()[:, None], dy.double()
-    n, g = (x.double() - m) * r, dy64 * w64
-    sg, sgn = g.sum(1, keepdim=True) / H, (g * n).sum(1, keepdim=True) / H
-    e1 = F * (H + 5) * g.abs().sum(1, keepdim=True) / H
-    e2 = F * (H + 9) * (g * n).abs().sum(1, keepdim=True) / H
-    if dx is not None:
-        size = g.abs() + sg.abs() + (n * sgn).abs()
-        e = r * (e1 + n.abs() * e2 * (1 + 3 * F) + 9 * F * size)
-        close(dx, r * (g - sg - n * sgn), e, what + " dx")
-    if dweight is not None:
-        close(dweight, (dy64 * n).sum(0), F * (rows + 10) * (dy64 * n).abs().sum(0), what + " dweight")
-    if dbias is not None:
-        close(dbias, dy64.sum(0), F * (rows + 4) * dy64.abs().sum(0), what + " dbias")
 
 
 @pytest.mark.parametrize("types", TYPES, ids=lambda t: ids(t))
@@ -119,7 +74,7 @@ def test_backward(size, types):
     ws = moe.alloc_layer_norm_backward_workspace(rows, cols).fill_(0xFF)
     dx, dw, db = moe.layer_norm_backward(dy, x, w, mean, rstd, ws=ws)
     assert dw.dtype == P and db.dtype == P and dx.dtype == T
-    check_backward(dy, x, w, mean, rstd, dx, dw, db, str(size))
+    check_norm_backward(dy, x, w, mean, rstd, dx, dw, db, str(size))
     for lead, pad in ((0, 3), (1, 0), (8, 8)):
         out = Output(rows, cols, T, pad, lead)
         again = moe.layer_norm_backward(inside(dy, lead, pad), inside(x, pad, lead), w, mean, rstd, dx=out.view)
@@ -127,10 +82,10 @@ def test_backward(size, types):
         out.check_surroundings()
     none = moe.layer_norm_backward(dy, x, None, mean, rstd, bias=False)
     assert none[1] is None and none[2] is None
-    check_backward(dy, x, None, mean, rstd, none[0], None, None, "no weight")
+    check_norm_backward(dy, x, None, mean, rstd, none[0], None, None, "no weight")
     only = moe.layer_norm_backward(dy, x, None, mean, rstd)
     assert torch.equal(only[0], none[0]) and only[2].dtype == T
-    check_backward(dy, x, None, mean, rstd, None, None, only[2], "bias alone")
+    check_norm_backward(dy, x, None, mean, rstd, None, None, only[2], "bias alone")
     part = torch.empty_like(dw)
     moe.moe_layer_norm_backward(dy, x, w, mean, rstd, None, part, None, ws)
     assert torch.equal(part, dw), "dweight alone"
@@ -176,7 +131,7 @@ def test_a_constant_row_and_large_offsets():
     x = torch.full((3, 4096), 7.25, device="cuda")
     assert torch.equal(moe.layer_norm(x, w, b), b.expand(3, -1))
     x = 1000.0 + torch.randn((5, 4096), generator=g, device="cuda")
-    check_forward(x, w, b, EPS, moe.layer_norm(x, w, b), None, None, "offset")
+    check_norm(x, w, b, EPS, moe.layer_norm(x, w, b), None, None, "offset")
 
 
 def test_bad_rows_stay_alone():
