@@ -22,7 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoe_hotpath.so")
 SOURCES = ["api.hip", "layout.hip", "quant.hip", "gemm1.hip", "stage2.hip", "combine.hip",
            "route_topk.hip", "few_token.hip", "dense.hip", "dense_few.hip", "dense_tile_nt.hip", "dense_tile_nn.hip",
-           "dense_tile_tn.hip", "norm.hip"]
+           "dense_tile_tn.hip", "dense_tile_pair.hip", "norm.hip"]
 TRACE_LIB = os.path.join(PKG, "libmoe_hotpath_trace.so")
 CEILING_LIB = os.path.join(PKG, "libmoe_ceiling.so")
 CEILING_SOURCES = ["ceiling.hip"]

@@ -303,6 +303,8 @@ moe_status launch_tiles_nn(int dtype, bool aligned, const Plan& plan, const Prod
                            hipStream_t stream);
 moe_status launch_tiles_tn(int dtype, bool aligned, const Plan& plan, const Product& p, const Epilogue& e, float* part,
                            hipStream_t stream);
+moe_status launch_pair(int dtype, const Plan& plan_dw, const Product& dw, const Epilogue& e_dw, const Plan& plan_dx,
+                       const Product& dx, const Epilogue& e_dx, hipStream_t stream);
 moe_status launch_few(int dtype, bool aligned, const Product& p, const Epilogue& e, hipStream_t stream);
 
 }  // namespace moe

@@ -305,16 +305,19 @@ moe_status run_backward(const Backward& b, int64_t m, int64_t n, int64_t k, int 
                         int64_t dw_ld, void* ws, hipStream_t stream) {
     moe_status st = MOE_OK;
     const int rows = b.terms == 2 ? 2 * kTermRows : (int)m;
-    if (dx) {
-        const Product p{d, w, d_ld, w_ld, rows, (int)k, (int)n, 0, 0};
-        const Epilogue e{nullptr, nullptr, nullptr, dx, 0, 0, dx_ld, (int)k, MOE_ACT_NONE, (int)m};
-        st = run_product(kNN, dtype, rows_aligned(d, d_ld, n) && rows_aligned(w, w_ld, k), p, e, ws, stream, b.terms);
+    const Product p_dx{d, w, d_ld, w_ld, rows, (int)k, (int)n, 0, 0};
+    const Epilogue e_dx{nullptr, nullptr, nullptr, dx, 0, 0, dx_ld, (int)k, MOE_ACT_NONE, (int)m};
+    const bool fast_dx = dx && rows_aligned(d, d_ld, n) && rows_aligned(w, w_ld, k);
+    const Product p_dw{d, x, d_ld, x_ld, (int)n, (int)k, rows, 0, b.terms == 2 ? (int)m : 0};
+    const Epilogue e_dw{nullptr, nullptr, nullptr, dw, 0, 0, dw_ld, (int)k, MOE_ACT_NONE, (int)n};
+    const bool fast_dw = dw && rows_aligned(d, d_ld, n) && rows_aligned(x, x_ld, k);
+    if (fast_dx && fast_dw) {
+        const Plan plan_dx = plan_product(kNN, rows, k, n, true, b.terms), plan_dw = plan_product(kTN, n, k, rows, true, b.terms);
+        if (plan_dx.tile == 256 && plan_dw.tile == 256 && !plan_dx.joined && !plan_dw.joined)
+            return launch_pair(dtype, plan_dw, p_dw, e_dw, plan_dx, p_dx, e_dx, stream);
     }
-    if (dw && st == MOE_OK) {
-        const Product p{d, x, d_ld, x_ld, (int)n, (int)k, rows, 0, b.terms == 2 ? (int)m : 0};
-        const Epilogue e{nullptr, nullptr, nullptr, dw, 0, 0, dw_ld, (int)k, MOE_ACT_NONE, (int)n};
-        st = run_product(kTN, dtype, rows_aligned(d, d_ld, n) && rows_aligned(x, x_ld, k), p, e, ws, stream, b.terms);
-    }
+    if (dx) st = run_product(kNN, dtype, fast_dx, p_dx, e_dx, ws, stream, b.terms);
+    if (dw && st == MOE_OK) st = run_product(kTN, dtype, fast_dw, p_dw, e_dw, ws, stream, b.terms);
     return st;
 }
 

@@ -243,19 +243,19 @@ __device__ __forceinline__ bool tile_at(const TileArgs& t, int slot, Tile& w) {
     return true;
 }
 
-template <class T, class C, bool AT, bool BT, Rows ROWS, TileEnd END, bool PAIRED>
-__global__ void __launch_bounds__(C::kThreads, 2)
-tile_kernel(TileArgs t) {
+// One product's tiles, `slot_of(turn)` the place in the XCD's run of this workgroup's turn-th one; its arguments lie ARGS
+// bytes into the kernel's.
+template <class T, class C, bool AT, bool BT, Rows ROWS, TileEnd END, bool PAIRED, int ARGS, class SlotOf>
+__device__ __forceinline__ void walk(const TileArgs& t, uint8_t* lds, SlotOf&& slot_of) {
     typedef typename Vec<T>::x8 x8;
     constexpr int MI = C::MI, NJ = C::NJ;
     constexpr bool ALIGNED = ROWS == kAligned;
-    __shared__ __align__(16) uint8_t lds[C::LDS];
     const int lane = threadIdx.x % MOE_WAVE;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / MOE_WAVE);
     const int wm = wave / C::WN, wn = wave % C::WN;
-    int slot = blockIdx.x / kXcds;
+    int turn = 0;
     Tile w;
-    if (!tile_at<C, PAIRED>(t, slot, w)) return;
+    if (!tile_at<C, PAIRED>(t, slot_of(turn), w)) return;
 
     Loader<T, C::BM, C::A_LOADS, AT, ROWS, false> la;
     Loader<T, C::BN, C::B_LOADS, BT, ROWS, PAIRED> lb;
@@ -350,7 +350,7 @@ tile_kernel(TileArgs t) {
         // reload waits for every load in flight.
         int lane;
         asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(lane));
-        uint64_t segment = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+        uint64_t segment = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr() + ARGS;
         asm volatile("" : "+s"(segment));
         const auto* from = (const __attribute__((address_space(4))) TileArgs*)segment;
         TileArgs t;
@@ -485,8 +485,7 @@ tile_kernel(TileArgs t) {
             if constexpr (kTouch) touch_step();
         }
         const Tile done = w;
-        slot += gridDim.x / kXcds;
-        more = tile_at<C, PAIRED>(t, slot, w);
+        more = tile_at<C, PAIRED>(t, slot_of(++turn), w);
         if (!more) w.kbeg = w.kend = 0;
         begin(w);
         part(zero, zero, zero, at);
@@ -504,18 +503,55 @@ using Wide = TileCfg<256, 256, 2, 4>;
 using Narrow = TileCfg<128, 128, 2, 2>;
 
 template <class T, class C, bool AT, bool BT, Rows ROWS, TileEnd END, bool PAIRED>
+__global__ void __launch_bounds__(C::kThreads, 2) tile_kernel(TileArgs t) {
+    __shared__ __align__(16) uint8_t lds[C::LDS];
+    const int first = blockIdx.x / kXcds, step = gridDim.x / kXcds;
+    walk<T, C, AT, BT, ROWS, END, PAIRED, 0>(t, lds, [=](int turn) { return first + turn * step; });
+}
+
+// A backward pass's two products in one launch, dw = d^T x and then dx = d w: neither leaves a last round with most of the
+// workgroups idle.  Those that dw's last round left out (an XCD's from `left` on) begin with as many of dx's tiles as one of
+// dw's takes time for; the rest of them goes round as ever.  8192 x 7168 -> 4096: 1.75 rounds of 128 steps and 3.5 of 64 are
+// 7 of 64 and not 8.
+struct PairArgs {
+    TileArgs dw, dx;
+    int ahead;               // dx's tiles to one of dw's
+};
+
+template <class T>
+__global__ void __launch_bounds__(Wide::kThreads, 2) pair_kernel(PairArgs t) {
+    __shared__ __align__(16) uint8_t lds[Wide::LDS];
+    const int me = blockIdx.x / kXcds, all = gridDim.x / kXcds;
+    walk<T, Wide, true, true, kAligned, kPlain, false, offsetof(PairArgs, dw)>(t.dw, lds,
+                                                                              [=](int turn) { return me + turn * all; });
+    __syncthreads();
+    const int per = (t.dw.total + kXcds - 1) / kXcds;
+    const int tiles = max(0, min(per, t.dw.total - (int)(blockIdx.x % kXcds) * per)), left = tiles % all;
+    const int ahead = left ? t.ahead : 0, free = all - left;
+    walk<T, Wide, false, true, kAligned, kPlain, false, offsetof(PairArgs, dx)>(t.dx, lds, [=](int turn) {
+        if (me < left) return ahead * free + turn * all + me;
+        return turn < ahead ? turn * free + me - left : ahead * free + (turn - ahead) * all + me;
+    });
+}
+
+template <class C, bool PAIRED>
+bool tile_args(const Plan& plan, const Product& p, const Epilogue& e, float* part, TileArgs* t) {
+    t->p = p, t->e = e, t->part = part, t->part_step = (int64_t)p.m * p.n;
+    t->kper = plan.kper, t->splits = plan.splits;
+    t->tiles_m = (p.m + C::BM - 1) / C::BM;
+    const int columns = PAIRED ? p.inter : p.n, width = PAIRED ? C::BN / 2 : C::BN;
+    t->tiles_n = (columns + width - 1) / width;
+    const int64_t total = (int64_t)t->tiles_m * t->tiles_n * plan.splits;
+    t->total = (int)total;
+    return total < (1 << 30);
+}
+
+template <class T, class C, bool AT, bool BT, Rows ROWS, TileEnd END, bool PAIRED>
 moe_status launch_tile(const Plan& plan, const Product& p, const Epilogue& e, float* part, hipStream_t stream) {
     TileArgs t;
-    t.p = p, t.e = e, t.part = part, t.part_step = (int64_t)p.m * p.n;
-    t.kper = plan.kper, t.splits = plan.splits;
-    t.tiles_m = (p.m + C::BM - 1) / C::BM;
-    const int columns = PAIRED ? p.inter : p.n, width = PAIRED ? C::BN / 2 : C::BN;
-    t.tiles_n = (columns + width - 1) / width;
-    const int64_t total = (int64_t)t.tiles_m * t.tiles_n * plan.splits;
-    if (total >= (1 << 30)) return MOE_ERR_UNSUPPORTED;
-    t.total = (int)total;
-    hipLaunchKernelGGL((tile_kernel<T, C, AT, BT, ROWS, END, PAIRED>), dim3(std::min((t.total + kXcds - 1) / kXcds * kXcds, kCus * C::kPerCu)),
-                       dim3(C::kThreads), 0, stream, t);
+    if (!tile_args<C, PAIRED>(plan, p, e, part, &t)) return MOE_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL((tile_kernel<T, C, AT, BT, ROWS, END, PAIRED>),
+                       dim3(std::min((t.total + kXcds - 1) / kXcds * kXcds, kCus * C::kPerCu)), dim3(C::kThreads), 0, stream, t);
     return launch_status();
 }
 
