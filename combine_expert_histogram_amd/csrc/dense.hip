@@ -7,32 +7,42 @@ bool rows_aligned(const void* p, int64_t ld, int64_t contiguous) {
     return ((uintptr_t)p & 15) == 0 && ld % 8 == 0 && contiguous % 8 == 0;
 }
 
-// The tile and the number of parts of K, by an estimate of the time (us).  A step of 64 of K takes 128 x 128 tiles 0.7 us
-// with one workgroup to a CU and 0.9 with two (rows that start anywhere 0.95 and 1.25), 256 x 256 tiles 1.2 with up to half
-// of the CUs at work (their clock is higher) and 1.45 with all; parts cost a launch and a pass over their sums, 6.5 us, 0.6 a
-// part and their bytes at 5 TB/s.  Fitted to 96 products (x w^T, dx and dw, 16 shapes from 100 x 1000 x 1000 to 8000 x 2000 x
-// 64 and 4096 x 4096 x 4096, rows aligned and not), of which it takes the fastest form or one within 7 % but for three: 128
-// tiles in one part take 1000 x 4096 x 4096 46 us, in two 52; 333 x 1408 x 4096 27 and, in four, 22.
+// The tile and the number of parts of K, by an estimate of the time.  A round of workgroups takes the tile's own time for
+// its first loads and its last stores, and a step of 64 of K so much with up to half of the places taken (one workgroup to a
+// CU where there is room for two; half of the CUs, at a higher clock, with 256 x 256) and so much with more; parts of K cost a
+// launch, a little a part, and a pass over their sums.  Fitted to 500 timings of 108 products (x w^T, dx and dw of 18 shapes
+// from 200 x 200 x 200 to 2048 x 7168 x 2048, rows aligned and not), which it meets to 11 %; what it takes of them is on
+// average 1 % over the fastest.  Some (us; 64, 128 and 256 tiles, best parts): 1001 x 777 x 1111 12.7, 20.8, 20.9; 100 x 1000
+// x 1000 7.7, 11.6, -; 2000 x 2000 x 2000 40.5, 33.2, 48.3; 2048 x 7168 x 2048 114, 62.5, 53.6; 300 x 300 x 8000 in one part
+// and six 44, 18.7.
+struct TileCost {
+    int tile, slots;
+    float once, half, full, half_anywhere, full_anywhere;    // us
+};
+constexpr TileCost kTileCosts[] = {
+    {64, 512, 1.75f, 0.33f, 0.49f, 0.54f, 0.67f}, {128, 512, 4.8f, 0.58f, 0.92f, 0.89f, 1.35f}, {256, 256, 8.8f, 1.1f, 1.42f, 0, 0}};
+constexpr float kJoin = 2.2f, kJoinPart = 0.53f, kJoinElement = 8 / 5.4e6f;    // 8 bytes at 5.4 TB/s
+
 Plan plan_product(Layout layout, int64_t m, int64_t n, int64_t k, bool aligned, int terms) {
     // (a launch holds less than 2^32 threads)
     if (layout == kNT && m <= 64 && n < (1 << 26)) return Plan{0, 1, (int)((k + kStepK - 1) / kStepK * kStepK), false};
     const uint32_t steps = (uint32_t)std::max<int64_t>((k + kStepK - 1) / kStepK, 1);     // no tokens: none for dw
-    Plan best{128, 1, 0, false};
+    Plan best{64, 1, 0, false};
     float least = 0.0f;
-    for (uint32_t tile = 128; tile <= (aligned ? 256u : 128u); tile *= 2) {
-        const int64_t tiles = (m + tile - 1) / tile * ((n + tile - 1) / tile);
-        const uint32_t slots = tile == 256 ? 256 : 512;
-        const float full = tile == 256 ? 1.45f : aligned ? 0.9f : 1.25f;
-        const float half = tile == 256 ? 1.2f : aligned ? 0.7f : 0.95f;
+    for (const TileCost& c : kTileCosts) {
+        if (c.tile == 256 && !aligned) break;
+        const int64_t tiles = (m + c.tile - 1) / c.tile * ((n + c.tile - 1) / c.tile);
+        const float half = aligned ? c.half : c.half_anywhere, full = aligned ? c.full : c.full_anywhere;
         for (uint32_t splits = 1; splits <= std::min(16u, std::max(1u, steps / 2)); ++splits) {
             const uint32_t per = (steps + splits - 1) / splits, parts = (steps + per - 1) / per;
-            const float join = parts > 1 ? 6.5f + 0.6f * parts + 1.6e-6f * parts * (float)(m * n) : 0.0f;
+            const float join = parts > 1 ? kJoin + parts * (kJoinPart + kJoinElement * (float)(m * n)) : 0.0f;
             if (best.kper && join >= least) break;
-            const int64_t all = tiles * parts, rest = all & (slots - 1);
-            const float us = join + per * ((float)(all / slots) * full + (rest > slots / 2 ? full : rest ? half : 0.0f));
+            const int64_t all = tiles * parts, rounds = all / c.slots, rest = all & (c.slots - 1);
+            const float us = join + (float)rounds * (c.once + per * full) +
+                             (rest > c.slots / 2 ? c.once + per * full : rest ? c.once + per * half : 0.0f);
             if (best.kper && us >= least) continue;
             least = us;
-            best = Plan{(int)tile, (int)parts, (int)(per * kStepK), false};
+            best = Plan{c.tile, (int)parts, (int)(per * kStepK), false};
         }
     }
     best.joined = best.splits > 1 || (terms == 2 && layout == kNN);
@@ -98,7 +108,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(JoinArgs t) {
             add_parts(t, row * t.n + t.inter + c, u, n);
             finish_gated<T>(t.e, row, c, v, u, n);
         } else {
-            finish<T>(t.e, row, c, v, n, residual_of<T>(t.e, row, c, n));
+            finish<T>(t.e, row, c, v, n, bias_of<T>(t.e, c, n), residual_of<T>(t.e, row, c, n));
         }
     }
 }

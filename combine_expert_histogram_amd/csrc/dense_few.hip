@@ -42,7 +42,7 @@ __device__ __forceinline__ void finish_tokens(const FewArgs& t, const float* sum
         }
         const int n = min(8, most - n0 - c);
         if constexpr (PAIRED) finish_gated<T>(t.e, token, n0, v, u, n);
-        else finish<T>(t.e, token, n0 + c, v, n, residual_of<T>(t.e, token, n0 + c, n));
+        else finish<T>(t.e, token, n0 + c, v, n, bias_of<T>(t.e, n0 + c, n), residual_of<T>(t.e, token, n0 + c, n));
     }
 }
 

@@ -381,8 +381,9 @@ __device__ __forceinline__ void walk(const TileArgs& t, uint8_t* lds, SlotOf&& s
             const int row = row_at(piece, h);
             return residual_of<T>(t.e, row, col, row < t.p.m ? n : 0);
         };
-        x8 res[2][kRows];
+        x8 res[2][kRows], bias;
         if constexpr (END == kPlain) {
+            bias = bias_of<T>(t.e, col, n);
 #pragma unroll
             for (int h = 0; h < kRows; ++h) res[0][h] = residual(0, h);
         }
@@ -423,7 +424,7 @@ __device__ __forceinline__ void walk(const TileArgs& t, uint8_t* lds, SlotOf&& s
                                 if (x < n) to[x] = v[x];
                         }
                     } else {
-                        finish<T>(t.e, row, col, v, n, res[piece & 1][h]);
+                        finish<T>(t.e, row, col, v, n, bias, res[piece & 1][h]);
                     }
                 }
             }
@@ -501,6 +502,7 @@ __device__ __forceinline__ void walk(const TileArgs& t, uint8_t* lds, SlotOf&& s
 
 using Wide = TileCfg<256, 256, 2, 4>;
 using Narrow = TileCfg<128, 128, 2, 2>;
+using Small = TileCfg<64, 64, 4, 1>;
 
 template <class T, class C, bool AT, bool BT, Rows ROWS, TileEnd END, bool PAIRED>
 __global__ void __launch_bounds__(C::kThreads, 2) tile_kernel(TileArgs t) {
@@ -559,10 +561,12 @@ template <class T, bool AT, bool BT, TileEnd END, bool PAIRED>
 moe_status launch_rows(bool aligned, const Plan& plan, const Product& p, const Epilogue& e, float* part, hipStream_t stream) {
     if (aligned) {
         if (plan.tile == 256) return launch_tile<T, Wide, AT, BT, kAligned, END, PAIRED>(plan, p, e, part, stream);
+        if (plan.tile == 64) return launch_tile<T, Small, AT, BT, kAligned, END, PAIRED>(plan, p, e, part, stream);
         return launch_tile<T, Narrow, AT, BT, kAligned, END, PAIRED>(plan, p, e, part, stream);
     }
     if (std::min(AT ? p.m : p.k, BT ? p.n : p.k) < 8)
-        return launch_tile<T, Narrow, AT, BT, kTiny, END, PAIRED>(plan, p, e, part, stream);
+        return launch_tile<T, Small, AT, BT, kTiny, END, PAIRED>(plan, p, e, part, stream);
+    if (plan.tile == 64) return launch_tile<T, Small, AT, BT, kAnywhere, END, PAIRED>(plan, p, e, part, stream);
     return launch_tile<T, Narrow, AT, BT, kAnywhere, END, PAIRED>(plan, p, e, part, stream);
 }
 
