@@ -23,9 +23,15 @@ constexpr TileCost kTileCosts[] = {
     {64, 512, 1.75f, 0.33f, 0.49f, 0.54f, 0.67f}, {128, 512, 4.8f, 0.58f, 0.92f, 0.89f, 1.35f}, {256, 256, 8.8f, 1.1f, 1.42f, 0, 0}};
 constexpr float kJoin = 2.2f, kJoinPart = 0.53f, kJoinElement = 8 / 5.4e6f;    // 8 bytes at 5.4 TB/s
 
+// Whether the weights are read in tiles of 16 rows, K cut among wavefronts, or as tiles of an ordinary product.  us at
+// rows x n x K, 16-row tiles / square ones: aligned 17 x 8192 x 8192 31 / 38, 64 x 8192 x 8192 39 / 40, 64 x 32768 x 2048
+// 37 / 38, 64 x 2048 x 8192 25 / 21; rows that start anywhere 8 x 8192 x 8192 43 / 42, 8 x 4096 x 7168 23 / 26, 1 of them
+// 18 / 26, 17 x 8192 x 8192 44 / 42, 64 x 4096 x 7168 38 / 29, 8 x 32768 x 2048 58 / 38.
+bool few_rows(int64_t m, int64_t n, int64_t k, bool aligned) {
+    return aligned ? m <= 64 && n < (1 << 26) : m <= 16 && n < 16384 && k >= 8;}
+
 Plan plan_product(Layout layout, int64_t m, int64_t n, int64_t k, bool aligned, int terms) {
-    // (a launch holds less than 2^32 threads)
-    if (layout == kNT && m <= 64 && n < (1 << 26)) return Plan{0, 1, (int)((k + kStepK - 1) / kStepK * kStepK), false};
+    if (layout == kNT && few_rows(m, n, k, aligned)) return Plan{0, 1, (int)((k + kStepK - 1) / kStepK * kStepK), false};
     const uint32_t steps = (uint32_t)std::max<int64_t>((k + kStepK - 1) / kStepK, 1);     // no tokens: none for dw
     Plan best{64, 1, 0, false};
     float least = 0.0f;
@@ -90,6 +96,7 @@ __device__ __forceinline__ void add_part(const float* p, float (&v)[8], int n) {
 __device__ __forceinline__ void add_parts(const JoinArgs& t, int64_t at, float (&v)[8], int n) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+#pragma unroll 4
     for (int s = 0; s < t.splits; ++s) {
         add_part(t.part + s * t.step + at, v, n);
         if (t.term) add_part(t.part + s * t.step + t.term + at, v, n);

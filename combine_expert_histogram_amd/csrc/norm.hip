@@ -110,48 +110,47 @@ __global__ void __launch_bounds__(W == 1 ? 256 : W * MOE_WAVE) norm_kernel(NormA
     constexpr int kTeam = W * MOE_WAVE, kTeams = W == 1 ? 4 : 1;
     __shared__ float lds[2][W];
     const int i = W == 1 ? threadIdx.x % MOE_WAVE : threadIdx.x;
-    const int64_t step = (int64_t)gridDim.x * kTeams;
-    for (int64_t row = (int64_t)blockIdx.x * kTeams + (W == 1 ? threadIdx.x / MOE_WAVE : 0); row < t.rows; row += step) {
-        const T* x = static_cast<const T*>(t.x) + row * t.x_ld;
-        float f[V][8];
-        float sum = 0.0f;
+    const int64_t row = (int64_t)blockIdx.x * kTeams + (W == 1 ? threadIdx.x / MOE_WAVE : 0);
+    if (row >= t.rows) return;                               // whole wavefronts, where no barrier follows
+    const T* x = static_cast<const T*>(t.x) + row * t.x_ld;
+    float f[V][8];
+    float sum = 0.0f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = 8 * (kTeam * v + i);
-            loadf(x + c, t.cols - c, f[v]);
+    for (int v = 0; v < V; ++v) {
+        const int c = 8 * (kTeam * v + i);
+        loadf(x + c, t.cols - c, f[v]);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += f[v][e];
+    const float mean = row_sum<W>(sum, lds[0]) / (float)t.cols;
+    float sq = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int n = t.cols - 8 * (kTeam * v + i);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            f[v][e] = e < n ? f[v][e] - mean : 0.0f;
+            sq = fmaf(f[v][e], f[v][e], sq);
         }
+    }
+    const float rstd = 1.0f / sqrtf(row_sum<W>(sq, lds[1]) / (float)t.cols + t.eps);
+    T* y = static_cast<T*>(t.y) + row * t.y_ld;
 #pragma unroll
-        for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
+        const int c = 8 * (kTeam * v + i), n = t.cols - c;
+        if (n <= 0) continue;
+        float w[8], b[8];
+        if (t.w) loadf(static_cast<const P*>(t.w) + c, n, w);
+        if (t.b) loadf(static_cast<const P*>(t.b) + c, n, b);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum += f[v][e];
-        const float mean = row_sum<W>(sum, lds[0]) / (float)t.cols;
-        float sq = 0.0f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int n = t.cols - 8 * (kTeam * v + i);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                f[v][e] = e < n ? f[v][e] - mean : 0.0f;
-                sq = fmaf(f[v][e], f[v][e], sq);
-            }
-        }
-        const float rstd = 1.0f / sqrtf(row_sum<W>(sq, lds[1]) / (float)t.cols + t.eps);
-        T* y = static_cast<T*>(t.y) + row * t.y_ld;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = 8 * (kTeam * v + i), n = t.cols - c;
-            if (n <= 0) continue;
-            float w[8], b[8];
-            if (t.w) loadf(static_cast<const P*>(t.w) + c, n, w);
-            if (t.b) loadf(static_cast<const P*>(t.b) + c, n, b);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[v][e] = fmaf(f[v][e] * rstd, t.w ? w[e] : 1.0f, t.b ? b[e] : 0.0f);
-            storef(y + c, f[v], n);
-        }
-        if (i == 0) {
-            if (t.mean) t.mean[row] = mean;
-            if (t.rstd) t.rstd[row] = rstd;
-        }
+        for (int e = 0; e < 8; ++e) f[v][e] = fmaf(f[v][e] * rstd, t.w ? w[e] : 1.0f, t.b ? b[e] : 0.0f);
+        storef(y + c, f[v], n);
+    }
+    if (i == 0) {
+        if (t.mean) t.mean[row] = mean;
+        if (t.rstd) t.rstd[row] = rstd;
     }
 }
 
@@ -413,10 +412,20 @@ int grad_grid(int rows, int cols) {
 }
 
 template <class T, class P, int W, int V>
-moe_status launch_norm(const NormArgs& t, hipStream_t stream) {
+moe_status launch_norm(NormArgs t, hipStream_t stream) {
     const int rows = W == 1 ? 4 : 1, threads = W == 1 ? 256 : W * MOE_WAVE;
-    hipLaunchKernelGGL((norm_kernel<T, P, W, V>), dim3(std::min((t.rows + rows - 1) / rows, kMostGroups)), dim3(threads), 0,
-                       stream, t);
+    for (const int most = kMostGroups * rows; t.rows > most;) {
+        NormArgs first = t;
+        first.rows = most;
+        const moe_status st = launch_norm<T, P, W, V>(first, stream);
+        if (st != MOE_OK) return st;
+        t.x = static_cast<const T*>(t.x) + most * t.x_ld;
+        t.y = static_cast<T*>(t.y) + most * t.y_ld;
+        if (t.mean) t.mean += most;
+        if (t.rstd) t.rstd += most;
+        t.rows -= most;
+    }
+    hipLaunchKernelGGL((norm_kernel<T, P, W, V>), dim3((t.rows + rows - 1) / rows), dim3(threads), 0, stream, t);
     return launch_status();
 }
 

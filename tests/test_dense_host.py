@@ -121,7 +121,7 @@ def test_nothing_to_do_is_fine(L):
 
 
 def test_workspaces(L):
-    assert b.moe_linear_workspace(1, 7168, 2048) == 0 and b.moe_linear_workspace(64, 4096, 7168) == 0
+    assert b.moe_linear_workspace(1, 7168, 2048) == 0 and b.moe_linear_workspace(16, 4096, 7168) == 0
     assert b.moe_linear_workspace(16384, 7168, 2048) == 0 and b.moe_linear_workspace(0, 8, 8) == 0
     assert b.moe_gated_linear_workspace(16384, 2048, 7168) == 0
     for fn in (b.moe_linear_workspace, b.moe_gated_linear_workspace, b.moe_gated_linear_backward_workspace):

@@ -9,8 +9,8 @@ from test_kernel_registers import found  # noqa: F401  (the fixture)
 MOST = 4
 
 
-@pytest.mark.parametrize("kernel", ["tile_kernel", "few_kernel", "few_stream_kernel", "join_kernel", "gate_grad_kernel", "dz_kernel",
-                                    "norm_kernel", "norm_long_kernel", "norm_grad_kernel", "norm_grad_long_kernel",
+@pytest.mark.parametrize("kernel", ["tile_kernel", "pair_kernel", "few_anywhere_kernel", "few_stream_kernel", "join_kernel",
+                                    "gate_grad_kernel", "dz_kernel", "norm_kernel", "norm_long_kernel", "norm_grad_kernel", "norm_grad_long_kernel",
                                     "norm_columns_kernel", "join_columns_kernel"])
 def test_no_kernel_spills(found, kernel):  # noqa: F811
     these = [k for k in found if kernel in k[".name"]]

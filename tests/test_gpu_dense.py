@@ -42,6 +42,32 @@ def test_linear_exact(size, place, dtype):
     z.check_surroundings()
 
 
+# Few rows and many columns: the ones where a workgroup takes one, two or four tiles of 16 (of 2 x 8 gated), and where rows
+# that start anywhere change over to square tiles; one tile short of each bound, and past it.
+@pytest.mark.parametrize("place", PLACES, ids=ids)
+@pytest.mark.parametrize("n", [4095, 8176, 8200, 16368, 16391])
+@pytest.mark.parametrize("m", [1, 16, 17, 33, 49, 64])
+def test_few_rows_exact(m, n, place):
+    require_gpu()
+    dtype = HALF[(m + n) % 2]
+    say(f"few rows {m} {n} {place} {dtype}")
+    g = generator(m + 10 * n)
+    k, inter = 200, n // 2
+    x, w = integers(g, m, k, dtype), integers(g, n, k, dtype)
+    bias, res = integers(g, 1, n, dtype, 9)[0], integers(g, m, n, dtype, 9)
+    z64 = x.double() @ w.double().T
+    y, h = Output(m, n, dtype, place[1], place[0]), Output(m, inter, dtype, place[1], place[0])
+    xp, wp = placed(x, place), placed(w, place)
+    moe.linear(xp, wp, bias=bias, act="relu", residual=placed(res, place), out=y.view)
+    same(y.view, act64(z64 + bias.double(), "relu")[0] + res.double(), "y")
+    y.check_surroundings()
+    h64 = act64(z64[:, :inter], "relu")[0] * z64[:, inter:2 * inter]
+    assert float(h64.abs().max()) < 2 ** 16
+    moe.gated_linear(xp, wp[:2 * inter], act="relu", out=h.view)
+    same(h.view, h64, "h")
+    h.check_surroundings()
+
+
 @pytest.mark.parametrize("dtype", HALF, ids=ids)
 @pytest.mark.parametrize("place", PLACES, ids=ids)
 @pytest.mark.parametrize("size", linear_sizes(), ids=ids)

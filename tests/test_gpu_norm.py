@@ -174,3 +174,24 @@ def test_far_rows():
     assert torch.equal(moe.layer_norm(far, w, b), ref)
     moe.layer_norm(x, w, b, out=far)
     assert torch.equal(far, ref)
+
+
+@pytest.mark.parametrize("rows,cols", [((1 << 22) + 5, 3), ((1 << 20) + 3, 2056), ((1 << 20) + 3, 16392)], ids=ids)
+def test_many_rows(rows, cols):
+    """More rows than one launch has workgroups for."""
+    require_gpu()
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    g = generator(rows)
+    at = torch.tensor([0, 1, 1 << 20, rows - 2, rows - 1], device="cuda")
+    x[at] = normal(g, 5, cols, torch.bfloat16)
+    mean, rstd = torch.full((rows,), math.nan, device="cuda"), torch.full((rows,), math.nan, device="cuda")
+    moe.layer_norm(x, out=x, mean=mean, rstd=rstd)
+    g = generator(rows)
+    small = normal(g, 5, cols, torch.bfloat16)
+    m, r = torch.empty(5, device="cuda"), torch.empty(5, device="cuda")
+    assert torch.equal(x[at], moe.layer_norm(small, mean=m, rstd=r))
+    assert torch.equal(mean[at], m) and torch.equal(rstd[at], r)
+    keep = torch.ones(rows, dtype=torch.bool, device="cuda")
+    keep[at] = False
+    assert not x.any(1)[keep].any() and not mean[keep].any()
+    assert bool((rstd[keep] == rstd[2]).all()) and abs(float(rstd[2]) * math.sqrt(EPS) - 1) < 8 * F
