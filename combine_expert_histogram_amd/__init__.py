@@ -6,9 +6,10 @@ stage2 (silu(gate) * up with its fp8 quant, the grouped GEMM2), and the
 serving forms for a few tokens (the router's top-k, matrix-vector products over
 fp8 and 4-bit weights, the whole expert layer in two launches), and the dense
 half of the block (layer norm, the gated linear layer, the linear layer with
-its epilogue, each with its backward pass), are HIP kernels behind the C ABI in include/moe_hotpath.h (libmoe_hotpath.so, built
-in-tree by ``python -m combine_expert_histogram_amd.build``); ``binding`` is
-the ctypes layer that passes torch device tensors and torch's current stream.
+its epilogue, each with its backward pass), are HIP kernels behind the C ABI in
+include/moe_hotpath.h (libmoe_hotpath.so, built in-tree by ``python -m
+combine_expert_histogram_amd.build``); ``binding`` is the ctypes layer that
+passes torch device tensors and torch's current stream.
 """
 from .binding import (  # noqa: F401
     Dims, MoeError, alloc_gemm1_workspace, alloc_layout, combine, grouped_gemm1, lib, moe_capacity, moe_combine,

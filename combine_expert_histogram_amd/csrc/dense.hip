@@ -71,6 +71,8 @@ namespace {
 constexpr int kThreads = 256;
 
 // ---------------------------------------------------------------- the parts of K summed, then the epilogue
+// y = epilogue(sum over the parts), in the parts' order; eight columns of a row to a thread.  Bound by its launch, and by the
+// parts' bytes where there are many: 5.4 TB/s (the fit's constant above).
 struct JoinArgs {
     const float* part;
     int64_t step;            // floats of one part
@@ -160,7 +162,8 @@ __device__ __forceinline__ void store_terms(T* p, int64_t second, const float (&
     store8(p + second, rest, n);
 }
 
-// d[row, :] = [dh u act'(g), dh act(g)]: read and written once, 8 columns of a row to a thread
+// d[row, :] = [dh u act'(g), dh act(g)]: read and written once, 8 columns of a row to a thread.  Memory bound: 16384 x 2 x
+// 2048 bf16 51 us for 336 MB.
 struct GateGradArgs {
     const void* dh;
     const void* gu;
@@ -194,7 +197,8 @@ __global__ void __launch_bounds__(kThreads) gate_grad_kernel(GateGradArgs t) {
 }
 
 // dz = dy act'(z), kept for the products where `d` is not null, and its column sums over this workgroup's rows: a
-// workgroup takes 256 columns (8 to a thread) and every eighth row of its share to one of its eight groups of threads
+// workgroup takes 256 columns (8 to a thread) and every eighth row of its share to one of its eight groups of threads.
+// Memory bound: 8192 x 4096 bf16 43 us, 4.7 TB/s.
 constexpr int kColumns = 256, kRowGroups = kThreads * 8 / kColumns, kMaxRowParts = 128;
 
 struct DzArgs {

@@ -10,7 +10,10 @@
 //
 // What bounds it (16384 x 4096 x 7168 bf16, 256 x 256 tiles, counters): the matrix cores are busy 0.67 of the time at 1.95
 // GHz, the clock that the card's power leaves them; with all operands in the caches they are busy 0.79 of it at 1.81 GHz.
-// LDS is busy a quarter of the time.  Tried: 32 x 32 MFMAs (as fast), four wavefronts of 128 x 128 (0.55 busy: one
+// LDS is busy a quarter of the time.  It reads 1.4 GB, as often as tiles of this size have to from the XCDs' L2.  With 2048 of
+// K they are busy 0.54: a tile's sums go out in a burst from all CUs at once, about 7 us of 53 at a large copy's rate, 13
+// with a residual (held four and eight pieces ahead, and the next tile's first step not waiting for the stores: the same
+// times).  Tried: 32 x 32 MFMAs (as fast), four wavefronts of 128 x 128 (0.55 busy: one
 // wavefront a SIMD cannot multiply while its loads queue), four steps of 32 of K (as fast, slower along rows: half lines),
 // wavefront priorities (none), 128 x 128 tiles (0.8 of the rate).
 #pragma once
@@ -438,7 +441,7 @@ __device__ __forceinline__ void walk(const TileArgs& t, uint8_t* lds, SlotOf&& s
     // 7168 x 2048 with a residual 425 -> 412.  Across (dx, dw) it takes time: 692 -> 735 and 750 -> 758.
     constexpr bool kTouch = ALIGNED && C::kPerCu == 1 && !AT && !BT;
     constexpr std::integral_constant<int, kTouch> touches{};
-    constexpr int kAhead = 4 * kBK, kShareA = 4, kShareB = 8;
+    constexpr int kAhead = 3 * kBK, kShareA = 4, kShareB = 8;
     const uint8_t* touch_at = nullptr;
     int64_t touch_by = 0;
     int touch_left = 0;
@@ -479,7 +482,10 @@ __device__ __forceinline__ void walk(const TileArgs& t, uint8_t* lds, SlotOf&& s
         for (int i = 0; i < MI; ++i)
 #pragma unroll
             for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if constexpr (kTouch) touch_tile();
+        if constexpr (kTouch) {
+            touch_tile();
+            touch_step();                                    // counted on by the first step's wait, as by the others'
+        }
         for (int g = 0; g < w.steps - 2; ++g, at ^= 1) {
             part(zero, zero, touches, at);
             part(one, zero, touches, at);

@@ -9,6 +9,10 @@
 // stay in the registers of the threads that hold those columns, over all rows of a workgroup; each workgroup leaves one
 // row of partial sums, which a second launch adds up in a fixed order.  Rows longer than the registers hold are read
 // again for each pass (from the caches, mostly).
+//
+// Measured: 16384 x 7168 bf16 forward 91 us, 5.2 TB/s (a large copy reaches 5.1); backward with weights in fp32 145 us, 4.9
+// TB/s, and 6.4 us for the columns' join of 512 rows of partial sums; 777 x 1111 fp32 backward 7.4 and 4.1 us; a single row
+// of 7168 4.2 us, a launch and one way to memory and back.
 #include "dense.h"
 
 namespace moe {
@@ -104,7 +108,8 @@ struct NormArgs {
     float eps;
 };
 
-// W wavefronts to a row; V pieces of eight columns to a thread, piece v of thread i at column 8 (64 W v + i)
+// W wavefronts to a row; V pieces of eight columns to a thread, piece v of thread i at column 8 (64 W v + i).  A row to a
+// team: with rows in a loop, 16384 x 7168 took 98 us and not 91 (fewer loads in flight between rows).
 template <class T, class P, int W, int V>
 __global__ void __launch_bounds__(W == 1 ? 256 : W * MOE_WAVE) norm_kernel(NormArgs t) {
     constexpr int kTeam = W * MOE_WAVE, kTeams = W == 1 ? 4 : 1;
@@ -210,7 +215,8 @@ struct NormGradArgs {
 
 // A workgroup (W > 1) or a wavefront (W = 1, four to a workgroup) takes every gridDim-th row.  16-bit rows: the next row is
 // on its way while a row is worked on, and the weights wait in LDS (asked for again with each row, they would queue behind
-// the next row's loads).
+// the next row's loads: the row ahead without the weights in LDS was slower than neither).  Both, and the columns' sums joined
+// by sixteen teams, took 16384 x 7168 bf16 from 197 us to 147.
 template <class T, class P, int W, int V>
 __global__ void __launch_bounds__(W == 1 ? 256 : W * MOE_WAVE) norm_grad_kernel(NormGradArgs t) {
     constexpr int kTeam = W * MOE_WAVE, kTeams = W == 1 ? 4 : 1;
@@ -330,7 +336,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : W * MOE_WAVE) norm_grad_kernel(
     }
 }
 
-// dx of rows of any length, read twice
+// dx of rows of any length, read twice (dy and x of 16 bits; a workgroup of sixteen wavefronts to a row)
 template <class T, class P>
 __global__ void __launch_bounds__(1024) norm_grad_long_kernel(NormGradArgs t) {
     __shared__ float lds[2][16];
