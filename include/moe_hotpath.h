@@ -534,8 +534,9 @@ moe_status moe_linear_workspace(int32_t m, int32_t n, int32_t k, size_t* bytes);
  * Out: y [m, n];  z [m, n] if not NULL (moe_linear_backward reads it), of dtype;
  *      act and residual are taken on the fp32 value, not on the rounded z.
  * ws: at least moe_linear_workspace bytes, 16-byte aligned, no initialisation
- * (may be NULL if that is 0).  Strides below 2^22, m * n and m * k and n * k
- * below 2^40, else MOE_ERR_UNSUPPORTED (in all four products' calls).
+ * (may be NULL if that is 0).  m, n and k below 2^30, strides below 2^22, m * n
+ * and m * k and n * k below 2^40, else MOE_ERR_UNSUPPORTED (in the calls of all
+ * four products).
  */
 moe_status moe_linear(int32_t m, int32_t n, int32_t k, int32_t dtype, const void* x, int64_t x_stride,
                       const void* w, int64_t w_stride, const void* bias, int32_t act,
@@ -553,8 +554,10 @@ moe_status moe_linear_backward_workspace(int32_t m, int32_t n, int32_t k, int32_
  *      w [n, k] (x is not read if dw is not wanted, nor w if dx is not; NULL
  *      then).
  * Out: dx [m, k], dw [n, k], dbias [n], of dtype;  each NULL if not wanted.
- * dz is rounded to dtype for the two products (their matrix instructions take
- * 16 bits); dbias sums it in fp32.
+ * The products' matrix instructions take 16 bits: dz is rounded to dtype once
+ * for them where m > 64, and held as the sum of two numbers of dtype, which
+ * leaves next to nothing of the rounding, where m <= 64 and there is an
+ * activation.  dbias sums dz in fp32.
  * ws: at least moe_linear_backward_workspace bytes, 16-byte aligned, no
  * initialisation.
  */
@@ -590,7 +593,8 @@ moe_status moe_gated_linear_backward_workspace(int32_t m, int32_t inter, int32_t
  * In:  dh [m, inter];  gu [m, 2*inter] as kept;  x, w as above (x is not read
  *      if dw is not wanted, nor w if dx is not; NULL then).
  * Out: dx [m, hidden], dw [2*inter, hidden], of dtype;  each NULL if not wanted.
- * dg and du are rounded to dtype for the two products.
+ * For the two products dg and du are rounded to dtype where m > 64 and held as
+ * the sum of two numbers of dtype where m <= 64.
  * ws: at least moe_gated_linear_backward_workspace bytes, 16-byte aligned, no
  * initialisation.
  */
