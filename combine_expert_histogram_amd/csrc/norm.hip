@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : W * MOE_WAVE) norm_grad_kernel(
     }
 }
 
-// dx of rows of any length, read twice (dy and x of 16 bits; a workgroup of sixteen wavefronts to a row)
+// dx of rows of any length, read twice; a workgroup of sixteen wavefronts to a row
 template <class T, class P>
 __global__ void __launch_bounds__(1024) norm_grad_long_kernel(NormGradArgs t) {
     __shared__ float lds[2][16];
@@ -409,12 +409,21 @@ Hold hold_of(int cols) {
     return Hold{16, 0};
 }
 
-// workgroups of the backward pass, each of which leaves a row of partial sums
+// In the backward pass eight wavefronts hold a row of 2049 .. 16384 columns: half the registers, twice the wavefronts on a CU
+// (2048 x 7168 bf16 28.6 us, with four 33.2; 16384 x 7168 145 and 145; 16384 x 4096 85 and 82).
+Hold grad_hold_of(int cols) {
+    if (cols <= 2048) return Hold{1, (cols + 511) / 512};
+    if (cols <= 16384) return Hold{8, cols <= 4096 ? 1 : cols <= 8192 ? 2 : 4};
+    return Hold{16, 0};
+}
+
+// Workgroups of the backward pass.  Each leaves a row of partial sums, to be written and read again, so that few rows are
+// better off with fewer: with 128, 256 and 512 of them 256 x 7168 takes 14.6, 19.0, - us, 2048 x 7168 35.9, 28.6, 32.5, 4096 x
+// 7168 59.8, 40.9, 43.5, 16384 x 7168 248, 149, 145, 4096 x 2048 21.6, 18.2, 18.9.
 int grad_grid(int rows, int cols) {
-    const Hold h = hold_of(cols);
+    const Hold h = grad_hold_of(cols);
     if (h.pieces == 0) return std::min(rows, 64);
-    if (h.waves == 1) return std::min((rows + 3) / 4, 512);
-    return std::min(rows, 512);
+    return std::min(h.waves == 1 ? (rows + 3) / 4 : rows, rows <= 512 ? 128 : rows < 8192 ? 256 : 512);
 }
 
 template <class T, class P, int W, int V>
@@ -462,7 +471,7 @@ moe_status run_norm(const NormArgs& t, hipStream_t stream) {
 
 template <class T, class P>
 moe_status run_grad(const NormGradArgs& t, void* dweight, void* dbias, hipStream_t stream) {
-    const Hold h = hold_of(t.cols);
+    const Hold h = grad_hold_of(t.cols);
     const int grid = grad_grid(t.rows, t.cols);
     moe_status st = MOE_OK;
     switch (h.waves * 8 + h.pieces) {
@@ -470,9 +479,8 @@ moe_status run_grad(const NormGradArgs& t, void* dweight, void* dbias, hipStream
         case 10: st = launch_grad<T, P, 1, 2>(t, stream); break;
         case 11: st = launch_grad<T, P, 1, 3>(t, stream); break;
         case 12: st = launch_grad<T, P, 1, 4>(t, stream); break;
-        case 34: st = launch_grad<T, P, 4, 2>(t, stream); break;
-        case 35: st = launch_grad<T, P, 4, 3>(t, stream); break;
-        case 36: st = launch_grad<T, P, 4, 4>(t, stream); break;
+        case 65: st = launch_grad<T, P, 8, 1>(t, stream); break;
+        case 66: st = launch_grad<T, P, 8, 2>(t, stream); break;
         case 68: st = launch_grad<T, P, 8, 4>(t, stream); break;
         default:
             // the columns first: dx may be dy or x itself

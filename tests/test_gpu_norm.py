@@ -18,6 +18,8 @@ SIZES = [(1, 1), (1, 7), (3, 8), (5, 63), (9, 512), (4, 513), (6, 1024), (1, 111
          (5, 5000), (1, 7168), (6, 8192), (3, 8193), (2, 16384), (3, 16385), (2, 40000), (777, 1111), (1030, 72), (2100, 136),
          (600, 4104)]
 EPS = 1e-5
+# rows to change the number of the backward pass's workgroups
+LONG = [(512, 2049), (513, 2049), (8191, 520), (8192, 520), (8192, 2560)]
 
 
 def stream(g, rows, cols, dtype):
@@ -60,7 +62,7 @@ def test_forward(size, types):
 
 
 @pytest.mark.parametrize("types", TYPES, ids=lambda t: ids(t))
-@pytest.mark.parametrize("size", SIZES, ids=ids)
+@pytest.mark.parametrize("size", SIZES + LONG, ids=ids)
 def test_backward(size, types):
     require_gpu()
     rows, cols = size
