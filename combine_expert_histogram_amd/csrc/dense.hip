@@ -10,18 +10,18 @@ bool rows_aligned(const void* p, int64_t ld, int64_t contiguous) {
 // The tile and the number of parts of K, by an estimate of the time.  A round of workgroups takes the tile's own time for
 // its first loads and its last stores, and a step of 64 of K so much with up to half of the places taken (one workgroup to a
 // CU where there is room for two; half of the CUs, at a higher clock, with 256 x 256) and so much with more; parts of K cost a
-// launch, a little a part, and a pass over their sums.  Fitted to 500 timings of 108 products (x w^T, dx and dw of 18 shapes
-// from 200 x 200 x 200 to 2048 x 7168 x 2048, rows aligned and not), which it meets to 11 %; what it takes of them is on
-// average 1 % over the fastest.  Some (us; 64, 128 and 256 tiles, best parts): 1001 x 777 x 1111 12.7, 20.8, 20.9; 100 x 1000
-// x 1000 7.7, 11.6, -; 2000 x 2000 x 2000 40.5, 33.2, 48.3; 2048 x 7168 x 2048 114, 62.5, 53.6; 300 x 300 x 8000 in one part
-// and six 44, 18.7.
+// launch, a little a part, and a pass over their sums.  Fitted to some 2500 timings of 213 products (x w^T, dx and dw of 40
+// shapes from 200 x 200 x 200 to 512 x 28672 x 4096, rows aligned and not, the weights from memory), which it meets to 13 %;
+// what it takes of them is on average 0.6 % over the fastest.  Some (us; 64, 128 and 256 tiles, best parts): 1001 x 777 x 1111
+// 12.7, 20.8, 20.9; 512 x 8192 x 8192 180, 95, 91; 1024 x 4096 x 7168 156, 91, 81; 1024 x 7168 x 2048 64, 34, 46; 2048 x 7168 x
+// 2048 112, 61, 53; 512 x 8192 x 8192 of 256 tiles in one part and four 183, 91.
 struct TileCost {
     int tile, slots;
     float once, half, full, half_anywhere, full_anywhere;    // us
 };
 constexpr TileCost kTileCosts[] = {
-    {64, 512, 1.75f, 0.33f, 0.49f, 0.54f, 0.67f}, {128, 512, 4.8f, 0.58f, 0.92f, 0.89f, 1.35f}, {256, 256, 8.8f, 1.1f, 1.42f, 0, 0}};
-constexpr float kJoin = 2.2f, kJoinPart = 0.53f, kJoinElement = 8 / 5.4e6f;    // 8 bytes at 5.4 TB/s
+    {64, 512, 0.6f, 0.52f, 0.56f, 0.63f, 0.72f}, {128, 512, 3.5f, 0.68f, 1.0f, 0.97f, 1.4f}, {256, 256, 6.9f, 1.2f, 1.4f, 0, 0}};
+constexpr float kJoin = 4.8f, kJoinPart = 0.38f, kJoinElement = 8 / 7.1e6f;    // 8 bytes, partly from the last cache
 
 // Whether the weights are read in tiles of 16 rows, K cut among wavefronts, or as tiles of an ordinary product.  us at
 // rows x n x K, 16-row tiles / square ones: aligned 17 x 8192 x 8192 31 / 38, 64 x 8192 x 8192 39 / 40, 64 x 32768 x 2048
@@ -72,7 +72,7 @@ constexpr int kThreads = 256;
 
 // ---------------------------------------------------------------- the parts of K summed, then the epilogue
 // y = epilogue(sum over the parts), in the parts' order; eight columns of a row to a thread.  Bound by its launch, and by the
-// parts' bytes where there are many: 5.4 TB/s (the fit's constant above).
+// parts' bytes where there are many (the fit's constants above).
 struct JoinArgs {
     const float* part;
     int64_t step;            // floats of one part
