@@ -98,7 +98,7 @@ __device__ __forceinline__ void add_part(const float* p, float (&v)[8], int n) {
 __device__ __forceinline__ void add_parts(const JoinArgs& t, int64_t at, float (&v)[8], int n) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
     for (int s = 0; s < t.splits; ++s) {
         add_part(t.part + s * t.step + at, v, n);
         if (t.term) add_part(t.part + s * t.step + t.term + at, v, n);
@@ -107,8 +107,9 @@ __device__ __forceinline__ void add_parts(const JoinArgs& t, int64_t at, float (
 
 template <class T>
 __global__ void __launch_bounds__(kThreads) join_kernel(JoinArgs t) {
-    for (int64_t item = (int64_t)blockIdx.x * kThreads + threadIdx.x; item < t.items; item += (int64_t)gridDim.x * kThreads) {
-        const int64_t row = item / t.chunks;
+    for (int64_t item = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; item < t.items;
+         item += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t row = t.items <= UINT32_MAX ? (uint32_t)item / (uint32_t)t.chunks : item / t.chunks;
         const int c = (int)(item - row * t.chunks) * 8;
         const int n = min(8, t.e.n - c);
         float v[8], u[8];
@@ -138,8 +139,10 @@ moe_status run_product(Layout layout, int dtype, bool aligned, const Product& p,
     t.splits = plan.splits, t.n = p.n, t.inter = p.inter, t.e = e;
     t.chunks = (e.n + 7) / 8;
     t.items = (two ? e.rows : rows) * t.chunks;
-    if (dtype == MOE_BF16) hipLaunchKernelGGL(join_kernel<__bf16>, dim3(grid_of(t.items)), dim3(kThreads), 0, stream, t);
-    else hipLaunchKernelGGL(join_kernel<_Float16>, dim3(grid_of(t.items)), dim3(kThreads), 0, stream, t);
+    const int threads = t.items < 65536 ? MOE_WAVE : kThreads;           // few: on all of the CUs
+    const dim3 grid((int)std::min<int64_t>((t.items + threads - 1) / threads, 16384));
+    if (dtype == MOE_BF16) hipLaunchKernelGGL(join_kernel<__bf16>, grid, dim3(threads), 0, stream, t);
+    else hipLaunchKernelGGL(join_kernel<_Float16>, grid, dim3(threads), 0, stream, t);
     return launch_status();
 }
 
@@ -216,7 +219,7 @@ __global__ void __launch_bounds__(kThreads) dz_kernel(DzArgs t) {
     __shared__ float lds[kRowGroups][kColumns + 4];
     const int c = blockIdx.x * kColumns + (threadIdx.x % (kColumns / 8)) * 8, group = threadIdx.x / (kColumns / 8);
     const int n = min(8, t.n - c);
-    const int64_t first = blockIdx.y * t.rows, last = t.second ? kTermRows : min(t.m, first + t.rows);
+    const int64_t first = blockIdx.y * t.rows, last = min(t.second ? (int64_t)kTermRows : t.m, first + t.rows);
     float sum[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
@@ -254,12 +257,13 @@ __global__ void __launch_bounds__(kThreads) dz_kernel(DzArgs t) {
     t.sums[(int64_t)blockIdx.y * pad4(t.n) + col] = s;
 }
 
-int64_t row_parts(int64_t m) { return std::max<int64_t>(1, std::min<int64_t>((m + 63) / 64, kMaxRowParts)); }
+// rows of sixteen to a workgroup, two to a thread, as long as that is not too many rows of sums
+int64_t row_parts(int64_t m) { return std::min<int64_t>((std::max<int64_t>(m, kTermRows) + 15) / 16, kMaxRowParts); }
 
 template <class T>
 moe_status launch_dz(DzArgs t, void* dbias, hipStream_t stream) {
     const int64_t parts = row_parts(t.m);
-    t.rows = (t.m + parts - 1) / parts;
+    t.rows = (std::max<int64_t>(t.m, kTermRows) + parts - 1) / parts;
     hipLaunchKernelGGL(dz_kernel<T>, dim3((t.n + kColumns - 1) / kColumns, (int)parts), dim3(kThreads), 0, stream, t);
     moe_status st = launch_status();
     if (st != MOE_OK || !dbias) return st;
