@@ -97,6 +97,24 @@ def gated_sizes():
             (256, 128, 2048), (70, 40, 8200), (300, 517, 257), (1000, 264, 136), (4096, 1800, 200)]
 
 
+# dz and its column sums where the rows of a workgroup change: up to 64 rows, sixteen to a workgroup, and 128 workgroups
+@pytest.mark.parametrize("act", ["none", "relu"])
+@pytest.mark.parametrize("n", [8, 259, 520])
+@pytest.mark.parametrize("m", [1, 15, 16, 17, 63, 64, 65, 80, 81, 2047, 2048, 2049, 4100])
+def test_bias_gradient_exact(m, n, act):
+    require_gpu()
+    dtype = HALF[(m + n) % 2]
+    say(f"bias gradient {m} {n} {act} {dtype}")
+    g = generator(m + 10 * n)
+    k = 24
+    x, w, dy, z = integers(g, m, k, dtype), integers(g, n, k, dtype), integers(g, m, n, dtype), integers(g, m, n, dtype, 2)
+    dz = dy.double() * act64(z.double(), act)[1]
+    dx, dw, db = moe.linear_backward(dy, x, w, act=act, z=z)
+    same(db, dz.sum(0), "dbias")
+    same(dx, dz @ w.double(), "dx")
+    same(dw, dz.T @ x.double(), "dw")
+
+
 @pytest.mark.parametrize("dtype", HALF, ids=ids)
 @pytest.mark.parametrize("place", PLACES, ids=ids)
 @pytest.mark.parametrize("size", gated_sizes(), ids=ids)
