@@ -10,7 +10,7 @@
 // row of partial sums, which a second launch adds up in a fixed order.  Rows longer than the registers hold are read
 // again for each pass (from the caches, mostly).
 //
-// Measured: 16384 x 7168 bf16 forward 91 us, 5.2 TB/s (a large copy reaches 5.1); backward with weights in fp32 145 us, 4.9
+// Measured: 16384 x 7168 bf16 forward 91 us, 5.2 TB/s (a large copy reaches 5.1); backward with weights in fp32 142 us, 5.0
 // TB/s, and 6.4 us for the columns' join of 512 rows of partial sums; 777 x 1111 fp32 backward 7.4 and 4.1 us; a single row
 // of 7168 4.2 us, a launch and one way to memory and back.
 #include "dense.h"
