@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(W * MOE_WAVE) few_stream_kernel(FewArgs t) {
         const bool in[2] = {8 * chunk[0] < K - k0, 8 * chunk[1] < K - k0};
         unroll<kLoads>([&](auto i_) __attribute__((always_inline)) {
             constexpr int i = decltype(i_)::value;
-            load_to_lds<i * 1024>(at[i], bytes[i], in[i & 1] ? (i < 2 * R ? off_w : off_x)[i & 1] : 0x80000000u,
+            load_to_lds<i * 1024>(at[i], bytes[i], in[i & 1] ? (i < 2 * R ? off_w : off_x)[i & 1] : kNowhere,
                                   ring + place * kStage);
             at[i] += 64 * W;
         });

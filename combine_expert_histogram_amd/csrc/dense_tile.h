@@ -23,7 +23,7 @@
 namespace moe {
 namespace {
 
-constexpr int kBK = kStepK;                                  // of K a step
+constexpr int kBK = kStepK;
 
 template <int BM_, int BN_, int WM_, int WN_>
 struct TileCfg {
@@ -60,17 +60,12 @@ enum Rows { kAligned, kAnywhere, kTiny };
 //   of an MFMA operand (sixteen rows, four chunks) at a time lies in different 16 B columns of the 256 B that its banks span;
 //   K across (TR = true): K step k holds 2 W bytes, the 32 B piece p (sixteen rows) in slot p ^ turn(k); read by
 //   ds_read_b64_tr_b16, in which sixteen lanes take four K steps of a piece and come out with one row's four each.
-template <int W>
-__device__ __forceinline__ int turn(int k) {
-    return ((k & 3) | (k >> 3 & 3) << 2) & (W / 16 - 1);
-}
-
 template <class T, int W, int L, bool TR, Rows ROWS, bool PAIRED>
 struct Loader {
     static constexpr bool ALIGNED = ROWS == kAligned;
     typedef typename Vec<T>::x8 x8;
-    static constexpr int kChunks = TR ? W / 8 : kBK / 8;      // 16 B chunks of a row in LDS
-    static constexpr int kPer = 64 / kChunks;                // rows in LDS of a load: K steps (TR) or rows of the operand
+    typedef Lines<W, TR> At;
+    static constexpr int kPer = At::kPer;                    // rows in LDS of a load: K steps (TR) or rows of the operand
     const T* base;           // element (row0, k = 0) where TR; else row 0 of the operand
     int64_t ld;
     int row0, rows;          // the tile's first row; rows of the operand (PAIRED: of one half)
@@ -88,21 +83,16 @@ struct Loader {
     __device__ __forceinline__ int row_of(int r) const { return PAIRED ? row0 + (r >> 6) * 32 + (r & 31) : row0 + r; }
     __device__ __forceinline__ int64_t half_of(int r) const { return PAIRED && (r & 32) ? rows : 0; }
 
-    // the row in LDS and the chunk of it that lane `lane` brings with load i
-    __device__ __forceinline__ int line(int i) const { return (blk0 + i) * kPer + lane / kChunks; }
-    __device__ __forceinline__ int chunk(int i) const {
-        if constexpr (TR) return (lane % kChunks) ^ (turn<W>(line(i)) << 1);
-        else return (lane % kChunks) ^ swizzle(line(i));
-    }
+    __device__ __forceinline__ int line(int i) const { return At::line(blk0 + i, lane); }
+    __device__ __forceinline__ int chunk(int i) const { return At::chunk(blk0 + i, lane); }
 
     __device__ __forceinline__ void start(const void* p, int64_t ld_, int rows_, bool again, int wave, int lane_) {
         base = static_cast<const T*>(p);
         ld = ld_, rows = rows_, blk0 = wave * L, lane = lane_;
         kstep = again ? 0 : kBK, by = again ? 0 : TR ? kBK * ld : kBK;
-        if constexpr (ALIGNED) {
+        if constexpr (ALIGNED && !TR) {
 #pragma unroll
-            for (int i = 0; i < L; ++i)
-                off[i] = (uint32_t)(lane / kChunks) * (uint32_t)((int)ld * 2) + chunk(i) * 16;
+            for (int i = 0; i < L; ++i) off[i] = At::offset(blk0 + i, lane, (int)ld, 0);
         }
     }
     // the tile whose rows start at row0_, its K from kbeg to kend_; a tile without K gives zeros
@@ -111,17 +101,18 @@ struct Loader {
         if constexpr (ALIGNED) {
 #pragma unroll
             for (int i = 0; i < L; ++i) {
-                const int b = blk0 + i, step = (int)ld;
-                int n;                                       // elements in reach; none or a negative number: no row
+                const int b = blk0 + i;
+                int left;
                 if constexpr (TR) {
                     at[i] = base + (int64_t)(kbeg + b * kPer) * ld + row0;
-                    n = (kPer - 1) * step + min(W, rows - row0);
+                    left = rows - row0;
+                    off[i] = At::offset(b, lane, (int)ld, left);
                 } else {
                     const int r = row_of(b * kPer);
                     at[i] = base + (half_of(b * kPer) + r) * ld + kbeg;
-                    n = (min(kPer, rows - r) - 1) * step + min(kBK, kend - kbeg);
+                    left = rows - r;
                 }
-                bytes[i] = kend > kbeg ? max(n, 0) * 2 : 0;
+                bytes[i] = kend > kbeg ? max(At::reach((int)ld, left, kend - kbeg), 0) * 2 : 0;
             }
         }
     }
@@ -129,8 +120,7 @@ struct Loader {
     // load I's next piece into its place in the stage at `lds`; past the end of K come zeros
     template <int I>
     __device__ __forceinline__ void direct(uint32_t lds) {
-        const int k = TR ? lane / kChunks : chunk(I) * 8, left = kend - k0 - (TR ? (blk0 + I) * kPer : 0);
-        load_to_lds<I * 1024>(at[I], bytes[I], k < left ? off[I] : 0x80000000u, lds);
+        load_to_lds<I * 1024>(at[I], bytes[I], At::in_step(blk0 + I, lane, kend - k0) ? off[I] : kNowhere, lds);
         at[I] += by;
         if constexpr (I == L - 1) k0 += kstep;
     }
