@@ -34,8 +34,8 @@ struct Lines {
     // Bytes from the load's first element to the lane's, ld elements from line to line.  TR: none where the chunk lies past
     // the last `left` of the operand's rows (whole chunks of them), so that nothing behind a line's end is read.
     static constexpr uint32_t offset(int block, int lane, int ld, int left) {
-        if (TR && 8 * chunk(block, lane) >= left) return kNowhere;
-        return (uint32_t)(lane / kChunks) * (uint32_t)(ld * 2) + (uint32_t)chunk(block, lane) * 16;
+        const uint32_t at = (uint32_t)(lane / kChunks) * (uint32_t)(ld * 2) + (uint32_t)chunk(block, lane) * 16;
+        return TR && 8 * chunk(block, lane) >= left ? kNowhere : at;
     }
     // Elements that a load may reach from its first: TR, `left` rows of the operand from the tile's first, K bounded by
     // in_step; else `left` rows from the load's first (none or fewer: no row) and `kleft` of K from the part's first.

@@ -256,8 +256,8 @@ __device__ __forceinline__ void walk(const TileArgs& t, uint8_t* lds, SlotOf&& s
     lb.start(t.p.b, t.p.ldb, PAIRED ? t.p.inter : t.p.n, BT && t.p.b_rows, wave, lane);
     auto begin = [&](const Tile& w) __attribute__((always_inline)) {
         la.tile(w.m0, w.kbeg, w.kend);
-        if (BT && t.p.b_rows && w.kend) lb.tile(w.n0, 0, t.p.b_rows);
-        else lb.tile(w.n0, w.kbeg, w.kend);
+        const bool again = BT && t.p.b_rows && w.kend;
+        lb.tile(w.n0, again ? 0 : w.kbeg, again ? t.p.b_rows : w.kend);
     };
     begin(w);
 
