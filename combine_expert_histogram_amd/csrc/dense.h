@@ -200,15 +200,17 @@ __device__ __forceinline__ void activate_grad(const float (&z)[N], float (&a)[N]
 // out_a[c] (out_b[c]) = the sum of column c (half + c) over `parts` rows of `sums`, `ld` floats (a multiple of 4) apart; each
 // may be null.  64 columns to a workgroup, four to a thread, sixteen teams that take every sixteenth row: a fixed order.
 // 512 rows of 2 x 7168: 42 us with four teams and a column to a thread.
+constexpr int kMostGroups = 1 << 20;                         // of a launch, which holds less than 2^32 threads
+
 __host__ __device__ inline int64_t pad4(int64_t n) { return (n + 3) & ~int64_t(3); }
 
 template <class T>
-__global__ void __launch_bounds__(256) join_columns_kernel(const float* sums, int parts, int64_t ld, int half, int n, T* out_a,
-                                                           T* out_b) {
+__global__ void __launch_bounds__(256) join_columns_kernel(const float* sums, int parts, int64_t ld, int64_t from, int half, int n,
+                                                           T* out_a, T* out_b) {
     constexpr int kTeams = 16;
     __shared__ f32x4 lds[kTeams][16];
     const int lane = threadIdx.x % 16, team = threadIdx.x / 16;
-    const int64_t c = (int64_t)blockIdx.x * 64 + lane * 4;
+    const int64_t first = from + (int64_t)blockIdx.x * 64, c = first + lane * 4;
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
     if (c < ld) {
 #pragma unroll 8
@@ -217,7 +219,7 @@ __global__ void __launch_bounds__(256) join_columns_kernel(const float* sums, in
     lds[team][lane] = sum;
     __syncthreads();
     if (threadIdx.x >= 64) return;
-    const int64_t at = (int64_t)blockIdx.x * 64 + threadIdx.x;
+    const int64_t at = first + threadIdx.x;
     float s = 0.0f;
 #pragma unroll
     for (int t = 0; t < kTeams; ++t) s += reinterpret_cast<const float*>(lds[t])[threadIdx.x];
@@ -231,9 +233,13 @@ __global__ void __launch_bounds__(256) join_columns_kernel(const float* sums, in
 template <class T>
 inline moe_status join_columns(const float* sums, int parts, int64_t ld, int64_t half, int n, void* out_a, void* out_b,
                                hipStream_t stream) {
-    hipLaunchKernelGGL(join_columns_kernel<T>, dim3((unsigned)((ld + 63) / 64)), dim3(256), 0, stream, sums, parts, ld, (int)half,
-                       n, static_cast<T*>(out_a), static_cast<T*>(out_b));
-    return launch_status();
+    moe_status st = MOE_OK;
+    for (int64_t from = 0, groups = (ld + 63) / 64; groups > 0 && st == MOE_OK; groups -= kMostGroups, from += (int64_t)kMostGroups * 64) {
+        hipLaunchKernelGGL(join_columns_kernel<T>, dim3((unsigned)std::min<int64_t>(groups, kMostGroups)), dim3(256), 0, stream, sums,
+                           parts, ld, from, (int)half, n, static_cast<T*>(out_a), static_cast<T*>(out_b));
+        st = launch_status();
+    }
+    return st;
 }
 
 // ---------------------------------------------------------------- the epilogue of a product

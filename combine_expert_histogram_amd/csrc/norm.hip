@@ -400,7 +400,6 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(NormGradArgs t) {
 struct Hold {
     int waves, pieces;
 };
-constexpr int kMostGroups = 1 << 20;                         // of a launch, which holds less than 2^32 threads
 
 Hold hold_of(int cols) {
     if (cols <= 2048) return Hold{1, (cols + 511) / 512};

@@ -197,3 +197,19 @@ def test_many_rows(rows, cols):
     keep[at] = False
     assert not x.any(1)[keep].any() and not mean[keep].any()
     assert bool((rstd[keep] == rstd[2]).all()) and abs(float(rstd[2]) * math.sqrt(EPS) - 1) < 8 * F
+
+
+@pytest.mark.parametrize("cols", [1 << 25, (1 << 25) + 36, 1 << 29], ids=ids)
+def test_many_columns(cols):
+    """More columns' sums than one launch has workgroups for: 2^20 of 64, and past 2^32 threads.  With a mean of 0 and an
+    rstd of 1 a single row's gradients are products of two 16-bit numbers, exact in fp32."""
+    require_gpu()
+    say(f"columns {cols}")
+    g = generator(cols % 1000)
+    x = torch.randint(-128, 129, (1, cols), generator=g, device="cuda", dtype=torch.int16).to(torch.bfloat16)
+    dy = torch.randint(-128, 129, (1, cols), generator=g, device="cuda", dtype=torch.int16).to(torch.bfloat16)
+    dw, db = torch.full((cols,), math.nan, device="cuda"), torch.full((cols,), math.nan, device="cuda")
+    ws = moe.alloc_layer_norm_backward_workspace(1, cols)
+    moe.moe_layer_norm_backward(dy, x, None, torch.zeros(1, device="cuda"), torch.ones(1, device="cuda"), None, dw, db, ws)
+    assert torch.equal(dw, x[0].float() * dy[0].float())
+    assert torch.equal(db, dy[0].float())
