@@ -254,6 +254,7 @@ struct Epilogue {
     int n;                   // columns of y
     int act;
     int rows;                // of y
+    const float* unit = nullptr;     // not null: the sums are multiplied by it first (a power of two; see Peaks)
 };
 
 // n <= 8 columns from c of one row; bias and res: those of the bias and the residual, read beforehand
@@ -265,6 +266,21 @@ __device__ __forceinline__ typename Vec<T>::x8 residual_of(const Epilogue& e, in
 template <class T>
 __device__ __forceinline__ typename Vec<T>::x8 bias_of(const Epilogue& e, int c, int n) {
     return e.bias ? load8(static_cast<const T*>(e.bias) + c, n) : typename Vec<T>::x8{};
+}
+
+// Only gradients of fp16 have a unit: it is one elsewhere, unread.
+template <class T>
+__device__ __forceinline__ float unit_of(const Epilogue& e) {
+    if constexpr (std::is_same<T, _Float16>::value) return e.unit ? *e.unit : 1.0f;
+    return 1.0f;
+}
+
+template <class T>
+__device__ __forceinline__ void in_units(float (&v)[8], float unit) {
+    if constexpr (std::is_same<T, _Float16>::value) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= unit;
+    }
 }
 
 template <class T>

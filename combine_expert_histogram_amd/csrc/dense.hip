@@ -107,6 +107,7 @@ __device__ __forceinline__ void add_parts(const JoinArgs& t, int64_t at, float (
 
 template <class T>
 __global__ void __launch_bounds__(kThreads) join_kernel(JoinArgs t) {
+    const float unit = unit_of<T>(t.e);                      // gated ones, forward, have none
     for (int64_t item = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; item < t.items;
          item += (int64_t)gridDim.x * blockDim.x) {
         const int64_t row = t.items <= UINT32_MAX ? (uint32_t)item / (uint32_t)t.chunks : item / t.chunks;
@@ -114,6 +115,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(JoinArgs t) {
         const int n = min(8, t.e.n - c);
         float v[8], u[8];
         add_parts(t, row * t.n + c, v, n);
+        in_units<T>(v, unit);
         if (t.inter) {
             add_parts(t, row * t.n + t.inter + c, u, n);
             finish_gated<T>(t.e, row, c, v, u, n);
@@ -147,16 +149,83 @@ moe_status run_product(Layout layout, int dtype, bool aligned, const Product& p,
 }
 
 // ---------------------------------------------------------------- the activations' gradients
+// What fp16 cannot hold.  The products take a computed gradient in 16 bits.  In fp16 one below 2^-14 loses bits, one below
+// 2^-25 all of them, and a product of two fp16 values may be past its largest.  So fp16 gradients are scaled, all of a call's
+// by one power of two that takes the largest finite one (dz: the largest dy, |act'| < 1.14) to 2^14 .. 2^15, and the
+// products' sums back by its inverse: both exact.  What is left is off by its own rounding or by 2^-39 of the largest,
+// whichever is more.  bf16 has fp32's range and needs none of it.
+//
+// The largest one: a pass of its own over what the gradients are made of, a maximum to a workgroup, which the next kernel's
+// workgroups each join for themselves (maxima: the order does not matter); of [dg du]'s at most kScaledGroups, so that each
+// has some work for it (16384 x 2 x 2048: 55 us, with 16384 of them 57.5).  Memory bound, kPeakAhead pieces of a thread on
+// their way at a time: 16384 x 2 x 2048 50 us, 8192 x 4096 16 us; 24 x 4608 3.5 us, a launch.
+constexpr int kPeakGroups = 1024, kPeakAhead = 4, kScaledGroups = 4096;
+struct Peaks {
+    float* most;             // [groups]; null: no scale
+    float* unit;             // the inverse of the scale, for the products
+    int groups;
+};
+
+__device__ __forceinline__ float group_max(float v) {
+    __shared__ float lds[kThreads / MOE_WAVE];
+#pragma unroll
+    for (int s = MOE_WAVE / 2; s; s >>= 1) v = fmaxf(v, __shfl_xor(v, s));
+    if (threadIdx.x % MOE_WAVE == 0) lds[threadIdx.x / MOE_WAVE] = v;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kThreads / MOE_WAVE; ++i) v = fmaxf(v, lds[i]);
+    return v;
+}
+
+// The scale of this call's gradients, one workgroup leaving its inverse.
+template <class T>
+__device__ __forceinline__ float scale_of(const Peaks& p) {
+    if constexpr (!std::is_same<T, _Float16>::value) return 1.0f;
+    if (!p.most) return 1.0f;
+    float most = 0.0f;
+    for (int i = threadIdx.x; i < p.groups; i += kThreads) most = fmaxf(most, p.most[i]);
+    most = group_max(most);
+    const int up = most > 0.0f ? min(14 + 127 - (int)(__float_as_uint(most) >> 23), 126) : 0;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.unit = __uint_as_float((uint32_t)(127 - up) << 23);
+    return __uint_as_float((uint32_t)(127 + up) << 23);
+}
+
+// f(row, column, columns) of every piece of eight columns of [m, cols], each once over the grid
+template <class F>
+__device__ __forceinline__ void each_piece(int m, int cols, F&& f) {
+    const int chunks = (cols + 7) / 8;
+    const int64_t items = (int64_t)m * chunks, step = (int64_t)gridDim.x * kThreads;
+    auto piece = [&](int64_t at) __attribute__((always_inline)) {
+        const int64_t row = items <= UINT32_MAX ? (uint32_t)at / (uint32_t)chunks : at / chunks;
+        const int c = (int)(at - row * chunks) * 8;
+        f(row, c, min(8, cols - c));
+    };
+    int64_t item = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    for (; item + (kPeakAhead - 1) * step < items; item += kPeakAhead * step) {
+#pragma unroll
+        for (int a = 0; a < kPeakAhead; ++a) piece(item + a * step);
+    }
+    for (; item < items; item += step) piece(item);
+}
+
+__device__ __forceinline__ float peak_of(float most, const float (&d)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) most = fabsf(d[i]) < __builtin_inff() ? fmaxf(most, fabsf(d[i])) : most;
+    return most;
+}
+
 // Up to kTermRows rows, what the products take of a gradient d is two terms, its rounding to 16 bits and the rounding of
 // what that leaves: rows 0 .. 63 and 64 .. 127 of the workspace, zeros behind the last token.  As exact as d in fp32; with
 // one term the error of a few rows' products is off by chance from that of their own rounding to twice it and more (1
 // token, 64 x 64: 1 to 2.2 times; 64 tokens and more: 1.41).  It costs little: the second term are rows that the tile has
 // anyway.  More tokens take one term, which is what their matrix instructions cost once.
 template <class T>
-__device__ __forceinline__ void store_terms(T* p, int64_t second, const float (&d)[8], int n) {
+__device__ __forceinline__ void store_terms(T* p, int64_t second, const float (&gradient)[8], int n, float scale) {
+    float d[8], rest[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d[i] = std::is_same<T, _Float16>::value ? gradient[i] * scale : gradient[i];
     store8(p, d, n);
     if (!second) return;
-    float rest[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float first = (float)(T)d[i];
@@ -174,29 +243,50 @@ struct GateGradArgs {
     int64_t dh_ld, gu_ld, d_ld, items;
     int64_t second;          // elements to the second term, 0: one term
     int m, inter, chunks, act;
+    Peaks peaks;
 };
+
+// dg and du of a piece of `n` columns from c
+template <class T>
+__device__ __forceinline__ void gate_grad(const GateGradArgs& t, int64_t row, int c, int n, float (&dg)[8], float (&du)[8]) {
+    const T* gu = static_cast<const T*>(t.gu) + row * t.gu_ld + c;
+    const auto dh = load8(static_cast<const T*>(t.dh) + row * t.dh_ld + c, n);
+    const auto gv = load8(gu, n), uv = load8(gu + t.inter, n);
+    float g[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = (float)gv[i];
+    activate_grad(g, du, dg, t.act);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        dg[i] *= (float)dh[i] * (float)uv[i];
+        du[i] *= (float)dh[i];
+    }
+}
 
 template <class T>
 __global__ void __launch_bounds__(kThreads) gate_grad_kernel(GateGradArgs t) {
+    const float scale = scale_of<T>(t.peaks);
     for (int64_t item = (int64_t)blockIdx.x * kThreads + threadIdx.x; item < t.items; item += (int64_t)gridDim.x * kThreads) {
         const int64_t row = item / t.chunks;
-        const int c = (int)(item - row * t.chunks) * 8, n = min(8, t.inter - c), have = row < t.m ? n : 0;
-        const T* gu = static_cast<const T*>(t.gu) + row * t.gu_ld + c;
-        const auto dh = load8(static_cast<const T*>(t.dh) + row * t.dh_ld + c, have);
-        const auto gv = load8(gu, have), uv = load8(gu + t.inter, have);
-        float g[8], a[8], d[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = (float)gv[i];
-        activate_grad(g, a, d, t.act);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            d[i] *= (float)dh[i] * (float)uv[i];
-            a[i] *= (float)dh[i];
-        }
+        const int c = (int)(item - row * t.chunks) * 8, n = min(8, t.inter - c);
+        float dg[8], du[8];
+        gate_grad<T>(t, row, c, row < t.m ? n : 0, dg, du);
         T* to = static_cast<T*>(t.d) + row * t.d_ld + c;
-        store_terms(to, t.second, d, n);
-        store_terms(to + t.inter, t.second, a, n);
+        store_terms(to, t.second, dg, n, scale);
+        store_terms(to + t.inter, t.second, du, n, scale);
     }
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads) gate_peak_kernel(GateGradArgs t) {
+    float most = 0.0f;
+    each_piece(t.m, t.inter, [&](int64_t row, int c, int n) __attribute__((always_inline)) {
+        float dg[8], du[8];
+        gate_grad<T>(t, row, c, n, dg, du);
+        most = peak_of(peak_of(most, dg), du);
+    });
+    most = group_max(most);
+    if (threadIdx.x == 0) t.peaks.most[blockIdx.x] = most;
 }
 
 // dz = dy act'(z), kept for the products where `d` is not null, and its column sums over this workgroup's rows: a
@@ -212,11 +302,27 @@ struct DzArgs {
     int64_t dy_ld, z_ld, d_ld, m, rows;
     int64_t second;          // elements to the second term, 0: one term
     int n, act;
+    Peaks peaks;
 };
+
+template <class T>
+__global__ void __launch_bounds__(kThreads) dz_peak_kernel(DzArgs t) {
+    float most = 0.0f;
+    each_piece((int)t.m, t.n, [&](int64_t row, int c, int n) __attribute__((always_inline)) {
+        const auto dy = load8(static_cast<const T*>(t.dy) + row * t.dy_ld + c, n);
+        float d[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = (float)dy[i];
+        most = peak_of(most, d);
+    });
+    most = group_max(most);
+    if (threadIdx.x == 0) t.peaks.most[blockIdx.x] = most;
+}
 
 template <class T>
 __global__ void __launch_bounds__(kThreads) dz_kernel(DzArgs t) {
     __shared__ float lds[kRowGroups][kColumns + 4];
+    const float scale = scale_of<T>(t.peaks);
     const int c = blockIdx.x * kColumns + (threadIdx.x % (kColumns / 8)) * 8, group = threadIdx.x / (kColumns / 8);
     const int n = min(8, t.n - c);
     const int64_t first = blockIdx.y * t.rows, last = min(t.second ? (int64_t)kTermRows : t.m, first + t.rows);
@@ -240,7 +346,7 @@ __global__ void __launch_bounds__(kThreads) dz_kernel(DzArgs t) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) d[i] = (float)dy[i];
             }
-            if (t.d) store_terms(static_cast<T*>(t.d) + row * t.d_ld + c, t.second, d, n);
+            if (t.d) store_terms(static_cast<T*>(t.d) + row * t.d_ld + c, t.second, d, n, scale);
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum[i] += d[i];
         }
@@ -260,10 +366,18 @@ __global__ void __launch_bounds__(kThreads) dz_kernel(DzArgs t) {
 // rows of sixteen to a workgroup, two to a thread, as long as that is not too many rows of sums
 int64_t row_parts(int64_t m) { return std::min<int64_t>((std::max<int64_t>(m, kTermRows) + 15) / 16, kMaxRowParts); }
 
+int peak_groups(int64_t m, int64_t cols) {
+    return (int)std::min<int64_t>((m * ((cols + 7) / 8) + kThreads - 1) / kThreads, kPeakGroups);
+}
+
 template <class T>
 moe_status launch_dz(DzArgs t, void* dbias, hipStream_t stream) {
     const int64_t parts = row_parts(t.m);
     t.rows = (std::max<int64_t>(t.m, kTermRows) + parts - 1) / parts;
+    if (t.peaks.most) {
+        t.peaks.groups = peak_groups(t.m, t.n);
+        hipLaunchKernelGGL(dz_peak_kernel<T>, dim3(t.peaks.groups), dim3(kThreads), 0, stream, t);
+    }
     hipLaunchKernelGGL(dz_kernel<T>, dim3((t.n + kColumns - 1) / kColumns, (int)parts), dim3(kThreads), 0, stream, t);
     moe_status st = launch_status();
     if (st != MOE_OK || !dbias) return st;
@@ -307,34 +421,41 @@ int64_t product_bytes(Layout layout, int64_t m, int64_t n, int64_t k, int terms 
                     plan_bytes(plan_product(layout, m, n, k, false, terms), m, n));
 }
 
-// the backward passes' workspace: dz (or [dg du]) where it is computed, in one or two terms, the bias's column sums, and
-// the products' parts
+// the backward passes' workspace: dz (or [dg du]) where it is computed, in one or two terms, the maxima for its scale, the
+// bias's column sums, and the products' parts
 struct Backward {
     int terms;
-    int64_t sums, parts, bytes;
+    int64_t peaks, sums, parts, bytes;
 };
 Backward backward_of(int64_t m, int64_t n, int64_t k, bool computed) {
     Backward b;
     b.terms = computed && m <= kTermRows ? 2 : 1;
     const int64_t rows = b.terms == 2 ? 2 * kTermRows : m;
-    b.sums = computed ? pad(rows * pad8(n) * 2) : 0;
+    b.peaks = computed ? pad(rows * pad8(n) * 2) : 0;
+    b.sums = b.peaks + (computed ? pad((kPeakGroups + 1) * 4) : 0);
     b.parts = b.sums + pad(row_parts(m) * pad4(n) * 4);
     b.bytes = b.parts + std::max(product_bytes(kNN, rows, k, n, b.terms), product_bytes(kTN, n, k, rows, b.terms));
     return b;
+}
+
+Peaks peaks_at(const Backward& b, int dtype, uint8_t* ws) {
+    if (dtype != MOE_FP16) return Peaks{nullptr, nullptr, 0};
+    float* most = reinterpret_cast<float*>(ws + b.peaks);
+    return Peaks{most, most + kPeakGroups, 0};
 }
 
 // dx = d w and dw = d^T x, either of them left out where it is null.  Two terms: dx's are rows of one product, summed as
 // its parts are; dw's are two steps of K, of which x's rows are read in each.
 moe_status run_backward(const Backward& b, int64_t m, int64_t n, int64_t k, int dtype, const void* d, int64_t d_ld,
                         const void* x, int64_t x_ld, const void* w, int64_t w_ld, void* dx, int64_t dx_ld, void* dw,
-                        int64_t dw_ld, void* ws, hipStream_t stream) {
+                        int64_t dw_ld, const float* unit, void* ws, hipStream_t stream) {
     moe_status st = MOE_OK;
     const int rows = b.terms == 2 ? 2 * kTermRows : (int)m;
     const Product p_dx{d, w, d_ld, w_ld, rows, (int)k, (int)n, 0, 0};
-    const Epilogue e_dx{nullptr, nullptr, nullptr, dx, 0, 0, dx_ld, (int)k, MOE_ACT_NONE, (int)m};
+    const Epilogue e_dx{nullptr, nullptr, nullptr, dx, 0, 0, dx_ld, (int)k, MOE_ACT_NONE, (int)m, unit};
     const bool fast_dx = dx && rows_aligned(d, d_ld, n) && rows_aligned(w, w_ld, k);
     const Product p_dw{d, x, d_ld, x_ld, (int)n, (int)k, rows, 0, b.terms == 2 ? (int)m : 0};
-    const Epilogue e_dw{nullptr, nullptr, nullptr, dw, 0, 0, dw_ld, (int)k, MOE_ACT_NONE, (int)n};
+    const Epilogue e_dw{nullptr, nullptr, nullptr, dw, 0, 0, dw_ld, (int)k, MOE_ACT_NONE, (int)n, unit};
     const bool fast_dw = dw && rows_aligned(d, d_ld, n) && rows_aligned(x, x_ld, k);
     if (fast_dx && fast_dw) {
         const Plan plan_dx = plan_product(kNN, rows, k, n, true, b.terms), plan_dw = plan_product(kTN, n, k, rows, true, b.terms);
@@ -420,15 +541,17 @@ extern "C" moe_status moe_linear_backward(int32_t m, int32_t n, int32_t k, int32
     uint8_t* at = static_cast<uint8_t*>(ws);
     const void* d = dy;
     int64_t d_ld = dy_stride;
+    const bool kept = keeps && (dx || dw);
+    const Peaks peaks = kept ? peaks_at(b, dtype, at) : Peaks{nullptr, nullptr, 0};
     if (keeps || dbias) {
-        const bool kept = keeps && (dx || dw);
         const DzArgs t{dy, keeps ? z : nullptr, kept ? at : nullptr, dbias ? reinterpret_cast<float*>(at + b.sums) : nullptr,
-                       dy_stride, z_stride, pad8(n), m, 0, kept && b.terms == 2 ? kTermRows * pad8(n) : 0, n, act};
+                       dy_stride, z_stride, pad8(n), m, 0, kept && b.terms == 2 ? kTermRows * pad8(n) : 0, n, act, peaks};
         st = dtype == MOE_BF16 ? launch_dz<__bf16>(t, dbias, stream) : launch_dz<_Float16>(t, dbias, stream);
         if (st != MOE_OK) return st;
         if (kept) d = at, d_ld = pad8(n);
     }
-    return run_backward(b, m, n, k, dtype, d, d_ld, x, x_stride, w, w_stride, dx, dx_stride, dw, dw_stride, at + b.parts, stream);
+    return run_backward(b, m, n, k, dtype, d, d_ld, x, x_stride, w, w_stride, dx, dx_stride, dw, dw_stride, peaks.unit,
+                        at + b.parts, stream);
 }
 
 extern "C" moe_status moe_gated_linear_workspace(int32_t m, int32_t inter, int32_t hidden, size_t* bytes) {
@@ -492,11 +615,17 @@ extern "C" moe_status moe_gated_linear_backward(int32_t m, int32_t inter, int32_
     if (misplaced(ws, 16)) return MOE_ERR_INVALID_ARG;
     uint8_t* at = static_cast<uint8_t*>(ws);
     const bool two = b.terms == 2;
-    GateGradArgs t{dh, gu, at, dh_stride, gu_stride, pad8(n), 0, two ? kTermRows * pad8(n) : 0, m, inter, (inter + 7) / 8, act};
+    GateGradArgs t{dh, gu, at, dh_stride, gu_stride, pad8(n), 0, two ? kTermRows * pad8(n) : 0, m, inter, (inter + 7) / 8, act,
+                   peaks_at(b, dtype, at)};
     t.items = (int64_t)(two ? kTermRows : m) * t.chunks;
-    if (dtype == MOE_BF16) hipLaunchKernelGGL(gate_grad_kernel<__bf16>, dim3(grid_of(t.items)), dim3(kThreads), 0, stream, t);
-    else hipLaunchKernelGGL(gate_grad_kernel<_Float16>, dim3(grid_of(t.items)), dim3(kThreads), 0, stream, t);
+    if (dtype == MOE_BF16) {
+        hipLaunchKernelGGL(gate_grad_kernel<__bf16>, dim3(grid_of(t.items)), dim3(kThreads), 0, stream, t);
+    } else {
+        t.peaks.groups = peak_groups(t.m, t.inter);
+        hipLaunchKernelGGL(gate_peak_kernel<_Float16>, dim3(t.peaks.groups), dim3(kThreads), 0, stream, t);
+        hipLaunchKernelGGL(gate_grad_kernel<_Float16>, dim3(std::min(grid_of(t.items), kScaledGroups)), dim3(kThreads), 0, stream, t);
+    }
     if ((st = launch_status()) != MOE_OK) return st;
     return run_backward(b, m, n, hidden, dtype, at, pad8(n), x, x_stride, w, w_stride, dx, dx_stride, dw, dw_stride,
-                        at + b.parts, stream);
+                        t.peaks.unit, at + b.parts, stream);
 }

@@ -350,6 +350,8 @@ __device__ __forceinline__ void walk(const TileArgs& t, uint8_t* lds, SlotOf&& s
         t.e.bias = from->e.bias, t.e.res = from->e.res, t.e.z = from->e.z, t.e.y = from->e.y;
         t.e.res_ld = from->e.res_ld, t.e.z_ld = from->e.z_ld, t.e.y_ld = from->e.y_ld;
         t.e.n = from->e.n, t.e.act = from->e.act;
+        if constexpr (BT && END == kPlain) t.e.unit = from->e.unit;      // the backward pass's
+        const float unit = unit_of<T>(t.e);
         t.part = from->part, t.part_step = from->part_step;
         t.p.m = from->p.m, t.p.n = from->p.n, t.p.inter = from->p.inter;
         uint8_t* stage = lds + 2 * C::STAGE + wave * 4096;
@@ -417,6 +419,7 @@ __device__ __forceinline__ void walk(const TileArgs& t, uint8_t* lds, SlotOf&& s
                                 if (x < n) to[x] = v[x];
                         }
                     } else {
+                        if constexpr (BT) in_units<T>(v, unit);
                         finish<T>(t.e, row, col, v, n, bias, res[piece & 1][h]);
                     }
                 }

@@ -544,7 +544,7 @@ moe_status moe_linear(int32_t m, int32_t n, int32_t k, int32_t dtype, const void
                       void* y, int64_t y_stride, void* ws, size_t ws_bytes, void* hip_stream);
 
 /* Workspace bytes moe_linear_backward needs (host-only): dz where there is an
- * activation, partial sums of the products and of dbias. */
+ * activation (and its scale), partial sums of the products and of dbias. */
 moe_status moe_linear_backward_workspace(int32_t m, int32_t n, int32_t k, int32_t act, size_t* bytes);
 
 /*
@@ -554,10 +554,13 @@ moe_status moe_linear_backward_workspace(int32_t m, int32_t n, int32_t k, int32_
  *      w [n, k] (x is not read if dw is not wanted, nor w if dx is not; NULL
  *      then).
  * Out: dx [m, k], dw [n, k], dbias [n], of dtype;  each NULL if not wanted.
- * The products' matrix instructions take 16 bits: dz is rounded to dtype once
- * for them where m > 64, and held as the sum of two numbers of dtype, which
- * leaves next to nothing of the rounding, where m <= 64 and there is an
- * activation.  dbias sums dz in fp32.
+ * The products' matrix instructions take 16 bits.  With an activation, dz is
+ * rounded to dtype once for them where m > 64, and held as the sum of two
+ * numbers of dtype where m <= 64: off by 2^-8 (bf16) or 2^-11 (fp16) of itself
+ * with one, by 2^-16 or 2^-22 with two.  fp16's dz is scaled for that by one
+ * power of two, which takes the largest finite |dy| to 2^14 or more and leaves
+ * the results again, so that it neither overflows nor loses more than 2^-39 of
+ * the largest |dy|.  dbias sums dz in fp32.
  * ws: at least moe_linear_backward_workspace bytes, 16-byte aligned, no
  * initialisation.
  */
@@ -594,7 +597,8 @@ moe_status moe_gated_linear_backward_workspace(int32_t m, int32_t inter, int32_t
  *      if dw is not wanted, nor w if dx is not; NULL then).
  * Out: dx [m, hidden], dw [2*inter, hidden], of dtype;  each NULL if not wanted.
  * For the two products dg and du are rounded to dtype where m > 64 and held as
- * the sum of two numbers of dtype where m <= 64.
+ * the sum of two numbers of dtype where m <= 64, as moe_linear_backward's dz;
+ * fp16's power of two goes by the largest finite |dg| or |du|.
  * ws: at least moe_gated_linear_backward_workspace bytes, 16-byte aligned, no
  * initialisation.
  */
