@@ -214,24 +214,40 @@ __device__ __forceinline__ float peak_of(float most, const float (&d)[8]) {
     return most;
 }
 
-// Up to kTermRows rows, what the products take of a gradient d is two terms, its rounding to 16 bits and the rounding of
-// what that leaves: rows 0 .. 63 and 64 .. 127 of the workspace, zeros behind the last token.  As exact as d in fp32; with
-// one term the error of a few rows' products is off by chance from that of their own rounding to twice it and more (1
-// token, 64 x 64: 1 to 2.2 times; 64 tokens and more: 1.41).  It costs little: the second term are rows that the tile has
-// anyway.  More tokens take one term, which is what their matrix instructions cost once.
+// Up to kTermRows rows, what the products take of a gradient d is two terms: a 16-bit number a little nearer to zero than d,
+// and what that leaves, rounded to 16 bits (rows 0 .. 63 and 64 .. 127 of the workspace, zeros behind the last token).
+// Their sum is within 2^-16 of d in bf16, 2^-22 in fp16.  With one term the error of a few rows' products is off by chance
+// from that of their own rounding to twice it and more (1 token, 64 x 64: 1 to 2.2 times; 64 tokens and more: 1.41).  It costs
+// little: the second term are rows that the tile has anyway.  More tokens take one term, which is what their matrix
+// instructions cost once.  Both terms have d's sign and neither is zero (but for d below the type's reach), so that an
+// infinity in w or x comes out as one: rounded to nearest, the second term would be zero or point the other way, and the sum
+// inf - inf.
+__device__ __forceinline__ float nearer_to_zero(__bf16 v) {
+    return (float)__builtin_bit_cast(__bf16, (uint16_t)(__builtin_bit_cast(uint16_t, v) - 1));
+}
+__device__ __forceinline__ float nearer_to_zero(_Float16 v) {
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)(__builtin_bit_cast(uint16_t, v) - 1));
+}
+
 template <class T>
 __device__ __forceinline__ void store_terms(T* p, int64_t second, const float (&gradient)[8], int n, float scale) {
     float d[8], rest[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) d[i] = std::is_same<T, _Float16>::value ? gradient[i] * scale : gradient[i];
-    store8(p, d, n);
-    if (!second) return;
+    if (second) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float first = (float)(T)d[i];
-        rest[i] = __builtin_isfinite(first) ? d[i] - first : 0.0f;       // an infinity stays one
+        for (int i = 0; i < 8; ++i) {
+            rest[i] = d[i];                                  // of zeros, infinities and NaNs
+            if (d[i] == 0.0f || !__builtin_isfinite(d[i])) continue;
+            float first = (float)(T)d[i];
+            if (fabsf(first) >= fabsf(d[i])) first = nearer_to_zero((T)first);
+            if ((T)(d[i] - first) == (T)0.0f && first != 0.0f) first = nearer_to_zero((T)first);
+            rest[i] = d[i] - first;
+            d[i] = first;
+        }
+        store8(p + second, rest, n);
     }
-    store8(p + second, rest, n);
+    store8(p, d, n);
 }
 
 // d[row, :] = [dh u act'(g), dh act(g)]: read and written once, 8 columns of a row to a thread.  Memory bound: 16384 x 2 x

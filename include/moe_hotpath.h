@@ -557,7 +557,8 @@ moe_status moe_linear_backward_workspace(int32_t m, int32_t n, int32_t k, int32_
  * The products' matrix instructions take 16 bits.  With an activation, dz is
  * rounded to dtype once for them where m > 64, and held as the sum of two
  * numbers of dtype where m <= 64: off by 2^-8 (bf16) or 2^-11 (fp16) of itself
- * with one, by 2^-16 or 2^-22 with two.  fp16's dz is scaled for that by one
+ * with one, by 2^-16 or 2^-22 with two, which have its sign, so that an
+ * infinity in x or w stays one.  fp16's dz is scaled for that by one
  * power of two, which takes the largest finite |dy| to 2^14 or more and leaves
  * the results again, so that it neither overflows nor loses more than 2^-39 of
  * the largest |dy|.  dbias sums dz in fp32.

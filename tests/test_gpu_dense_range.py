@@ -141,6 +141,40 @@ def test_gradients_of_unlike_size(m):
         assert not torch.isfinite(got[0][m // 2]).any() and not torch.isfinite(got[1][5]).any()
 
 
+def same_infinities(got, want, what):
+    """Infinities and NaNs where the formula has them."""
+    for f in (torch.isnan, torch.isposinf, torch.isneginf):
+        assert torch.equal(f(got), f(want)), what
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", HALF, ids=ids)
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu"])
+@pytest.mark.parametrize("m", [1, 5, 64, 65])
+def test_infinite_weights_and_tokens(m, act, dtype):
+    """They meet gradients of 16 bits (whole numbers) and of more."""
+    require_gpu()
+    g = generator(m)
+    n, k = 24, 40
+    dy = torch.randint(1, 9, (m, n), generator=g, device="cuda").to(dtype)
+    dy = dy * (torch.randint(0, 2, (m, n), generator=g, device="cuda") * 2 - 1).to(dtype)
+    z = torch.randint(1, 4, (m, n), generator=g, device="cuda").to(dtype)
+    x, w = normal(g, m, k, dtype), normal(g, n, k, dtype)
+    x[m // 2, 5], w[3, 7], w[4, 9] = math.inf, math.inf, -math.inf
+    for t, u in ((dy, z), (torch.zeros_like(dy), z)):
+        dz = t.double() * act64(u.double(), act)[1]
+        dx, dw, _ = moe.linear_backward(t, x, w, act=act, z=u)
+        same_infinities(dx, dz @ w.double(), f"dx {m} {act}")
+        same_infinities(dw, dz.T @ x.double(), f"dw {m} {act}")
+    gu = torch.cat((z[:, :n // 2], dy[:, :n // 2]), 1)
+    dh = dy[:, n // 2:]
+    a, da = act64(gu[:, :n // 2].double(), act)
+    d = torch.cat((dh.double() * gu[:, n // 2:].double() * da, dh.double() * a), 1)
+    dx, dw = moe.gated_linear_backward(dh, x, w, gu, act=act)
+    same_infinities(dx, d @ w.double(), f"gated dx {m} {act}")
+    same_infinities(dw, d.T @ x.double(), f"gated dw {m} {act}")
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("m", [8, 200])
 def test_each_replay_takes_its_own_scale(m):
