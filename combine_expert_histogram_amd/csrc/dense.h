@@ -97,9 +97,9 @@ __device__ __forceinline__ void load_to_lds(const void* p, int bytes, uint32_t o
 // In fp32; the exponential and the reciprocal are the hardware's (a few ulps), unseen behind a rounding to 16 bits.
 //   silu      z s(z), s(z) = 1 / (1 + e^-z)
 //   gelu      z P(z), P the normal distribution's; below 0, where 1 + erf would cancel, P(-u) = e^(-u^2 / 2) g(u) with
-//             g(u) = e^(u^2 / 2) erfc(u / sqrt 2) / 2 = t Q(t), t = 1 / (1 + 3 u / 8), Q of degree 8 fitted to g to 2.3e-7 of it
-//             everywhere (weighted least squares, reweighted towards the largest error); above 0, 1 - P(-u).  The library's
-//             erfc took 1001 x 777 outputs from 18 us to 36.
+//             g(u) = e^(u^2 / 2) erfc(u / sqrt 2) / 2 = t Q(t), t = 1 / (1 + 3 u / 8), Q of degree 8 fitted to g (weighted
+//             least squares, reweighted towards the largest error), whose fp32 constants give it to 2.6e-7 of it everywhere,
+//             the most at 0; above 0, 1 - P(-u).  The library's erfc took 1001 x 777 outputs from 18 us to 36.
 //   gelu_tanh z (1 + tanh u) / 2 = z s(2u), u = sqrt(2 / pi) (z + 0.044715 z^3)
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
 // P(z); bell: e^(-z^2 / 2)
