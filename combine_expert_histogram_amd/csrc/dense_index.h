@@ -50,4 +50,29 @@ struct Lines {
     }
 };
 
+// ---------------------------------------------------------------- who takes which tile
+// Workgroup b runs on XCD b % 8; each XCD takes a run of a product's `total` tiles, its workgroups slots of that run.
+constexpr int kXcds = 8, kCus = 256;                         // of an MI355X
+
+constexpr int run_of(int total) { return (total + kXcds - 1) / kXcds; }
+
+// The tile in slot `slot` of XCD `xcd`'s run, and whether there is one; if not, none is in the slots behind it.
+constexpr int tile_of(int total, int xcd, int slot) { return xcd * run_of(total) + slot; }
+constexpr bool has_tile(int total, int xcd, int slot) { return slot < run_of(total) && tile_of(total, xcd, slot) < total; }
+
+// How many tiles XCD `xcd`'s run has.
+constexpr int tiles_of(int total, int xcd) {
+    const int run = run_of(total), rest = total - xcd * run, most = rest < run ? rest : run;
+    return most > 0 ? most : 0;
+}
+
+// The slot of turn `turn` in a second product's run, for an XCD's workgroup `me` of `all`: those that the first product's last
+// round left out (from `left` on) begin with `ahead` tiles each (none where its rounds are whole), the rest of the run goes
+// round as ever.
+constexpr int slot_behind(int me, int all, int left, int ahead, int turn) {
+    const int free = all - left;
+    if (me < left) return ahead * free + turn * all + me;
+    return turn < ahead ? turn * free + me - left : ahead * free + (turn - ahead) * all + me;
+}
+
 }  // namespace moe

@@ -48,8 +48,6 @@ struct TileArgs {
     int kper, splits, tiles_m, tiles_n, total;
 };
 
-constexpr int kXcds = 8, kCus = 256;                         // of an MI355X
-
 enum TileEnd { kPlain, kGated, kPart };
 // the operands' rows: whole 16-byte pieces on 16-byte boundaries; anywhere, eight elements and more; anything
 enum Rows { kAligned, kAnywhere, kTiny };
@@ -218,9 +216,8 @@ struct Tile {
 template <class C, bool PAIRED>
 __device__ __forceinline__ bool tile_at(const TileArgs& t, int slot, Tile& w) {
     constexpr int kGroup = 8;
-    const int per = (t.total + kXcds - 1) / kXcds;
-    const int id = (int)(blockIdx.x % kXcds) * per + slot;
-    if (slot >= per || id >= t.total) return false;
+    const int xcd = (int)(blockIdx.x % kXcds), id = tile_of(t.total, xcd, slot);
+    if (!has_tile(t.total, xcd, slot)) return false;
     const int tiles = t.tiles_m * t.tiles_n;
     w.split = id / tiles;
     const int in = id - w.split * tiles;
@@ -526,13 +523,9 @@ __global__ void __launch_bounds__(Wide::kThreads, 2) pair_kernel(PairArgs t) {
     walk<T, Wide, true, true, kAligned, kPlain, false, offsetof(PairArgs, dw)>(t.dw, lds,
                                                                               [=](int turn) { return me + turn * all; });
     __syncthreads();
-    const int per = (t.dw.total + kXcds - 1) / kXcds;
-    const int tiles = max(0, min(per, t.dw.total - (int)(blockIdx.x % kXcds) * per)), left = tiles % all;
-    const int ahead = left ? t.ahead : 0, free = all - left;
-    walk<T, Wide, false, true, kAligned, kPlain, false, offsetof(PairArgs, dx)>(t.dx, lds, [=](int turn) {
-        if (me < left) return ahead * free + turn * all + me;
-        return turn < ahead ? turn * free + me - left : ahead * free + (turn - ahead) * all + me;
-    });
+    const int left = tiles_of(t.dw.total, (int)(blockIdx.x % kXcds)) % all, ahead = left ? t.ahead : 0;
+    walk<T, Wide, false, true, kAligned, kPlain, false, offsetof(PairArgs, dx)>(
+        t.dx, lds, [=](int turn) { return slot_behind(me, all, left, ahead, turn); });
 }
 
 template <class C, bool PAIRED>

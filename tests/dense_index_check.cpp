@@ -40,7 +40,22 @@ int check(int waves, int rows, int K, int ld, int kper) {
     return 0;
 }
 
+// How often the workgroups of one launch take each tile of a product, the second of a pair's two where dw > 0.
+void walk(int total, int dw, int grid, int ahead, int* taken) {
+    for (int b = 0; b < grid; ++b) {
+        const int xcd = b % kXcds, me = b / kXcds, all = grid / kXcds;
+        const int left = tiles_of(dw, xcd) % all;
+        for (int turn = 0;; ++turn) {
+            const int slot = dw ? slot_behind(me, all, left, left ? ahead : 0, turn) : me + turn * all;
+            if (!has_tile(total, xcd, slot)) break;
+            ++taken[tile_of(total, xcd, slot)];
+        }
+    }
+}
+
 }  // namespace
+
+extern "C" void count_tiles(int total, int dw, int grid, int ahead, int* taken) { walk(total, dw, grid, ahead, taken); }
 
 extern "C" int check_loads(int width, int across, int rows, int K, int ld, int kper) {
     if (width == 256) return across ? check<256, 4, true>(8, rows, K, ld, kper) : check<256, 4, false>(8, rows, K, ld, kper);

@@ -38,3 +38,26 @@ def test_no_load_leaves_its_rows(index, rows, K, width, gap):
         # K along the rows: whole chunks of it, any number of rows
         bad = index.check_loads(width, 0, K, rows, rows + gap, kper)
         assert not bad, f"K along, parts of {kper}: a load {WRONG[bad]}"
+
+
+def taken(index, total, dw, grid, ahead):
+    counts = (ctypes.c_int * total)()
+    index.count_tiles(total, dw, grid, ahead, counts)
+    return set(counts)
+
+
+def test_every_tile_is_taken_once(index):
+    """By launches of as many workgroups as the host chooses, one and two to a CU."""
+    for total in [*range(1, 300), 448, 511, 512, 513, 1000, 2047, 4097]:
+        for most in (256, 512):
+            grid = min((total + 7) // 8 * 8, most)
+            assert taken(index, total, 0, grid, 0) == {1}, (total, grid)
+
+
+def test_every_tile_of_a_joint_launch_is_taken_once(index):
+    """The second product's, behind any number of the first's: whole rounds, short runs on the last XCDs, few tiles."""
+    for dw in [1, 7, 8, 9, 100, 145, 255, 256, 257, 297, 448, 493, 512, 561, 1000]:
+        assert taken(index, dw, 0, 256, 0) == {1}
+        for dx in [1, 5, 63, 64, 65, 145, 255, 256, 391, 493, 495, 1023, 2145]:
+            for ahead in (1, 2, 3, 4, 11, 100):
+                assert taken(index, dx, dw, 256, ahead) == {1}, (dw, dx, ahead)
