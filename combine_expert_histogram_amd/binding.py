@@ -644,6 +644,8 @@ def few_token_layer(d: Dims, inter: int, x, topk_ids, topk_w, w1: Weight, w2: We
 
 
 # ---------------------------------------------------------------- the dense half, forward and backward
+# None of these calls records anything for autograd: a tensor that requires gradients is taken as its values, and what
+# comes back has no history.  Gradients are the *_backward calls'.
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
